@@ -12,6 +12,7 @@ Sources (page title, section): "QLoRA: Efficient Finetuning of Quantized LLMs"
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -26,7 +27,7 @@ __all__ = [
     "Nf4Weight", "nf4_codebook", "nf4_quantize", "double_quant", "dequant", "quantize_weight",
     "qlora_linear_fwd", "qlora_linear_bwd", "nf4_recon_error", "rank_topk",
     "dense_linear_fwd", "dense_linear_bwd", "chanq_quantize", "chanq_linear_fwd", "chanq_linear_bwd", "chanq_learn",
-    "workspace_size", "check", "set_wait_timeout_ns", "Qnf4Error",
+    "grad_norm", "clip_grad_norm", "workspace_size", "check", "set_wait_timeout_ns", "Qnf4Error",
 ]
 
 
@@ -447,6 +448,70 @@ def loftq_nf4(W: torch.Tensor, r: int, steps: int = 5, ws=None):
               scale2.data_ptr(), mean.data_ptr(), A.data_ptr(), B.data_ptr(), errs.data_ptr(),
               wsb.data_ptr(), wsb.numel(), _stream(W))
     return Nf4Weight(N, K, packed, code2, scale2, mean[:1]), A, B, errs
+
+
+_GRAD_DTYPES = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}
+
+
+def _grad_list(ts, what: str):
+    """Host arrays (pointers, dtypes, element counts) of a list of gradients."""
+    for t in ts:
+        if t.dtype not in _GRAD_DTYPES:
+            raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be CUDA tensors")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+    if len({t.device for t in ts}) > 1:
+        raise ValueError(f"{what} must be on one device")
+    return (array("Q", [t.data_ptr() for t in ts]), array("i", [_GRAD_DTYPES[t.dtype] for t in ts]),
+            array("q", [t.numel() for t in ts]))
+
+
+def _grad_call(grads, n: int, norm, ws, max_norm=None, out=None):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("the list of gradients is empty")
+    ptr, dt, num = _grad_list(grads, "gradients")
+    dev = grads[0].device
+    if norm is None:
+        norm = torch.empty(n, dtype=torch.float32, device=dev)
+    elif _req(norm, torch.float32, "norm").numel() != n or norm.device != dev:
+        raise ValueError(f"norm must hold {n} values on {dev}")
+    a = [v.buffer_info()[0] for v in (ptr, dt, num)]
+    args = (len(grads), *a, n)
+    if out is not None:
+        optr, odt, onum = _grad_list(out, "outputs")
+        if odt != dt or onum != num or out[0].device != dev:
+            raise ValueError("one output per gradient, of its dtype, size and device")
+        live = [p for p, m in zip(optr, num) if m]
+        if len(set(live)) != len(live):
+            raise ValueError("an output appears twice")
+        args += (float(max_norm), optr.buffer_info()[0])
+    with torch.cuda.device(dev):
+        wsb = _ws(int(lib.qnf4_grad_workspace_size(len(grads), a[2], n)), grads[0], ws)
+        _lib.call("qnf4_grad_norm" if out is None else "qnf4_clip_grad_norm", *args, norm.data_ptr(),
+                  wsb.data_ptr(), wsb.numel() * wsb.element_size(), _stream(grads[0]))
+    return norm
+
+
+def grad_norm(grads, n: int = 1, norm=None, ws=None) -> torch.Tensor:
+    """The 2-norm of every adapter's gradient over a list of fp32 or bf16 tensors: fp32 [n].
+    Each tensor is n equal contiguous parts, part a belonging to adapter a (the layout of dA
+    [n, r, K] and dB [n, N, r]); n = 1 gives the global norm. Summed in float64, in a fixed
+    order."""
+    return _grad_call(grads, n, norm, ws)
+
+
+def clip_grad_norm(grads, max_norm: float, n: int = 1, out=None, norm=None, ws=None):
+    """Gradients scaled by min(1, max_norm / (norm + 1e-6)) of their adapter: (the list of
+    scaled tensors, the norms fp32 [n] before scaling). grads and n as in ``grad_norm``. out
+    is a list of buffers of the same sizes and dtypes; pass ``grads`` itself to scale in place
+    (then a part whose factor is 1 is not touched). Each adapter has its own factor, so one
+    whose gradient is infinite or NaN leaves the others as they should be."""
+    grads = list(grads)
+    out = [torch.empty_like(g) for g in grads] if out is None else list(out)
+    return out, _grad_call(grads, n, norm, ws, max_norm, out)
 
 
 def check(stream: int | None = None) -> None:

@@ -69,6 +69,9 @@ SIGNATURES = {
                                    P, P, SZ, P]),
     "qnf4_chanq_learn": (ST, [P, I64, I64, I32, P, I32, P, P, P, P, P]),
     "qnf4_loftq_nf4": (ST, [P, I64, I64, I32, I32, P, P, P, P, P, P, P, P, SZ, P]),
+    "qnf4_grad_workspace_size": (SZ, [I32, P, I32]),
+    "qnf4_grad_norm": (ST, [I32, P, P, P, I32, P, P, SZ, P]),
+    "qnf4_clip_grad_norm": (ST, [I32, P, P, P, I32, F32, P, P, P, SZ, P]),
     "qnf4_workspace_size": (SZ, [I32, I64, I64, I64, I32]),
     "qnf4_check": (ST, [P]),
     "qnf4_set_wait_timeout_ns": (ST, [C.c_uint64]),

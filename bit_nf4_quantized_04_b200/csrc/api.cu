@@ -24,6 +24,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "gemm.cuh"
+#include "grad.cuh"
 #include "loftq.cuh"
 #include "quant.cuh"
 #include "tables.h"
@@ -1062,6 +1063,97 @@ LoftqLayout loftq_layout(int64_t N, int64_t K, int r) {
   return l;
 }
 
+// ---------------------------------------------------------------------------
+// Gradient norms and clipping over a list of tensors (see grad.cuh)
+// ---------------------------------------------------------------------------
+// Pieces of one adapter's part over the whole list.
+int64_t grad_pieces(int32_t count, const int64_t* elems, int32_t n) {
+  int64_t p = 0;
+  for (int32_t t = 0; t < count; ++t) p += (elems[t] / n + kGradPiece - 1) / kGradPiece;
+  return p;
+}
+
+size_t grad_ws_bytes(int32_t count, const int64_t* elems, int32_t n) {
+  return align256(static_cast<size_t>(grad_pieces(count, elems, n)) * n * sizeof(double)) +
+         align256(static_cast<size_t>(n) * sizeof(float));
+}
+
+qnf4_status check_grad_args(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                            int32_t n, void* const* out, const float* norm) {
+  if (count < 0) return fail(QNF4_ERR_ARG, "count must be >= 0 (got %d)", count);
+  if (n < 1) return fail(QNF4_ERR_ARG, "n must be positive (got %d)", n);
+  if (count > 0 && (!g || !dtype || !elems)) return fail(QNF4_ERR_ARG, "NULL array");
+  if (!norm) return fail(QNF4_ERR_ARG, "NULL norm");
+  if (!al16(norm)) return fail(QNF4_ERR_ALIGN, "norm must be 16-byte aligned");
+  for (int32_t t = 0; t < count; ++t) {
+    if (dtype[t] != QNF4_OUT_F32 && dtype[t] != QNF4_OUT_BF16)
+      return fail(QNF4_ERR_ARG, "tensor %d: dtype must be fp32 or bf16", t);
+    if (elems[t] < 0 || elems[t] % n)
+      return fail(QNF4_ERR_SHAPE, "tensor %d: %lld elements are not %d equal parts", t, (long long)elems[t], n);
+    if (elems[t] == 0) continue;
+    if (!g[t] || (out && !out[t])) return fail(QNF4_ERR_ARG, "tensor %d: NULL buffer", t);
+    const uintptr_t es = dtype[t] == QNF4_OUT_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(g[t]) % es || (out && reinterpret_cast<uintptr_t>(out[t]) % es))
+      return fail(QNF4_ERR_ALIGN, "tensor %d: not aligned to its element size", t);
+  }
+  return QNF4_OK;
+}
+
+// The launches' table of tensors [t0, t0 + count).
+void grad_tab(GradTab* tab, int32_t t0, int32_t count, const void* const* g, const int32_t* dtype,
+              const int64_t* elems, int32_t n, void* const* out, int64_t base, int64_t pieces) {
+  std::memset(tab->bf16, 0, sizeof(tab->bf16));
+  tab->count = count;
+  tab->n = n;
+  tab->base = base;
+  tab->pieces = pieces;
+  tab->piece0[0] = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const int32_t t = t0 + i;
+    tab->in[i] = g[t];
+    tab->out[i] = out ? out[t] : nullptr;
+    tab->part[i] = elems[t] / n;
+    tab->piece0[i + 1] = tab->piece0[i] + (tab->part[i] + kGradPiece - 1) / kGradPiece;
+    if (dtype[t] == QNF4_OUT_BF16) tab->bf16[i >> 5] |= 1u << (i & 31);
+  }
+}
+
+qnf4_status grad_norm_clip(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                           int32_t n, float max_norm, void* const* out, float* norm, void* ws,
+                           size_t ws_bytes, cudaStream_t s) {
+  if (!ws || !al16(ws) || ws_bytes < grad_ws_bytes(count, elems, n))
+    return fail(QNF4_ERR_WORKSPACE, "workspace too small or not 16-byte aligned (%zu < %zu)", ws_bytes,
+                grad_ws_bytes(count, elems, n));
+  const int64_t pieces = grad_pieces(count, elems, n);
+  double* sums = static_cast<double*>(ws);
+  float* coef = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                         align256(static_cast<size_t>(pieces) * n * sizeof(double)));
+  static thread_local GradTab tab;  // 16 KB: kept off the stack
+  int launches = 0;
+  auto pass = [&](bool scale) {
+    int64_t base = 0;
+    for (int32_t t0 = 0; t0 < count; t0 += kGradMaxTensors) {
+      grad_tab(&tab, t0, std::min(kGradMaxTensors, count - t0), g, dtype, elems, n, out, base, pieces);
+      const int64_t per = tab.piece0[tab.count];
+      base += per;
+      if (per == 0) continue;
+      const int64_t ctas = (per * n + kGradWarps - 1) / kGradWarps;
+      const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ctas, num_sms() * 8)));
+      if (scale)
+        launch_pdl(k_grad_scale, grid, dim3(32 * kGradWarps), 0, s, tab, static_cast<const float*>(coef));
+      else
+        launch_pdl(k_grad_sq, grid, dim3(32 * kGradWarps), 0, s, tab, sums);
+      ++launches;
+    }
+  };
+  pass(false);
+  launch_pdl(k_grad_norm, dim3(static_cast<unsigned>(n)), dim3(512), 0, s, static_cast<const double*>(sums),
+             pieces, max_norm, norm, out ? coef : static_cast<float*>(nullptr));
+  ++launches;
+  if (out) pass(true);
+  return launched(out ? "clip_grad_norm" : "grad_norm", launches);
+}
+
 }  // namespace
 }  // namespace qnf4
 
@@ -1793,6 +1885,32 @@ qnf4_status qnf4_chanq_linear_bwd(const uint8_t* packed, const int64_t* row_off,
     if (st != QNF4_OK) return st;
   }
   return linear_bwd(src, x, dY, M, A, B, r, scale, dX, dA, dB, ws, own, s);
+}
+
+size_t qnf4_grad_workspace_size(int32_t count, const int64_t* elems, int32_t n) {
+  if (count < 0 || n < 1 || (count > 0 && !elems)) return 0;
+  return grad_ws_bytes(count, elems, n);
+}
+
+qnf4_status qnf4_grad_norm(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                           int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_grad_norm");
+  qnf4_status st = check_grad_args(count, g, dtype, elems, n, nullptr, norm);
+  if (st != QNF4_OK) return st;
+  return grad_norm_clip(count, g, dtype, elems, n, 0.f, nullptr, norm, ws, ws_bytes,
+                        static_cast<cudaStream_t>(stream));
+}
+
+qnf4_status qnf4_clip_grad_norm(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                                int32_t n, float max_norm, void* const* out, float* norm, void* ws,
+                                size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_clip_grad_norm");
+  if (!(max_norm >= 0.f) || std::isinf(max_norm)) return fail(QNF4_ERR_ARG, "max_norm must be finite and >= 0");
+  if (!out) return fail(QNF4_ERR_ARG, "NULL out");
+  qnf4_status st = check_grad_args(count, g, dtype, elems, n, out, norm);
+  if (st != QNF4_OK) return st;
+  return grad_norm_clip(count, g, dtype, elems, n, max_norm, out, norm, ws, ws_bytes,
+                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -353,6 +353,32 @@ QNF4_API qnf4_status qnf4_loftq_nf4(const void* W_bf16, int64_t N, int64_t K, in
                            float* mean, float* A, float* B, double* errs, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* [QLoRA opening formula: A and B are all that is trained] The 2-norm of each adapter's
+ * gradient over a list of tensors. Tensor t has elems[t] elements (0 is allowed) of dtype[t]
+ * (QNF4_OUT_F32 or QNF4_OUT_BF16) and is n equal contiguous parts, part a belonging to
+ * adapter a (the layout of dA [n, r, K] and dB [n, N, r]; n = 1 gives the global norm):
+ *   norm[a] = sqrt(sum over t and over part a of tensor t of g^2)    (device, fp32 [n]).
+ * The squares are summed in float64 and in a fixed order, so no finite gradient overflows on
+ * the way and equal calls give equal bits. g, dtype and elems are host arrays of `count`
+ * entries (0 gives norms of 0); the tensors need only be aligned to their element size.
+ * Workspace: qnf4_grad_workspace_size(count, elems, n). Errors: QNF4_ERR_ARG for NULL or a
+ * dtype other than the two, QNF4_ERR_SHAPE where elems[t] is not a multiple of n. */
+QNF4_API size_t qnf4_grad_workspace_size(int32_t count, const int64_t* elems, int32_t n);
+QNF4_API qnf4_status qnf4_grad_norm(int32_t count, const void* const* g, const int32_t* dtype,
+                           const int64_t* elems, int32_t n, float* norm, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* The norms above, and the list scaled by them:
+ *   out[t] = g[t] * c[a],  c[a] = min(1, max_norm / (norm[a] + 1e-6)),
+ * in the tensors' own dtypes (one rounding). out[t] is g[t] itself (in place; parts whose
+ * factor is 1 are then not touched) or a buffer that overlaps none of the list's tensors, and
+ * no two outputs overlap. An infinite norm gives the factor 0 (0 * inf entries become NaN), a
+ * NaN norm a NaN factor, for that adapter alone. max_norm is finite and >= 0. */
+QNF4_API qnf4_status qnf4_clip_grad_norm(int32_t count, const void* const* g, const int32_t* dtype,
+                                const int64_t* elems, int32_t n, float max_norm,
+                                void* const* out, float* norm, void* ws, size_t ws_bytes,
+                                void* stream);
+
 /* Bytes of device workspace an operation needs for these sizes (0 if none). */
 QNF4_API size_t qnf4_workspace_size(int32_t op, int64_t N, int64_t K, int64_t M, int32_t r);
 

@@ -1,0 +1,73 @@
+"""The argument checks of the many-adapter calls and of gradient clipping, without a GPU: every
+call here is refused on the host, before a launch and before any pointer is read."""
+import ctypes as C
+
+import pytest
+import torch
+
+FAKE = 1 << 20  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def q():
+    import __graft_entry__
+    __graft_entry__.build()
+    import bit_nf4_quantized_04_b200 as q
+    return q
+
+
+def _grad_args(ptrs=(FAKE, FAKE), dtypes=(0, 1), elems=(12, 24)):
+    k = len(ptrs)
+    keep = ((C.c_void_p * k)(*ptrs), (C.c_int32 * k)(*dtypes), (C.c_int64 * k)(*elems))
+    return keep, [C.addressof(a) for a in keep]
+
+
+def test_grad_norm_refusals(q):
+    f = q.lib.qnf4_grad_norm
+    keep, a = _grad_args()
+    assert f(-1, *a, 1, FAKE, FAKE, 1 << 20, None) == 1
+    assert f(2, *a, 0, FAKE, FAKE, 1 << 20, None) == 1
+    assert f(2, None, a[1], a[2], 1, FAKE, FAKE, 1 << 20, None) == 1
+    assert f(2, *a, 1, None, FAKE, 1 << 20, None) == 1
+    assert f(2, *a, 1, FAKE + 4, FAKE, 1 << 20, None) == 3
+    assert f(2, *a, 5, FAKE, FAKE, 1 << 20, None) == 2       # 12 elements are not 5 parts
+    assert f(2, *a, 4, FAKE, FAKE, 16, None) == 6
+    assert f(2, *a, 4, FAKE, None, 1 << 20, None) == 6
+    keep, a = _grad_args(dtypes=(0, 2))
+    assert f(2, *a, 1, FAKE, FAKE, 1 << 20, None) == 1
+    keep, a = _grad_args(ptrs=(FAKE, None))
+    assert f(2, *a, 1, FAKE, FAKE, 1 << 20, None) == 1
+    keep, a = _grad_args(ptrs=(FAKE + 2, FAKE))              # an fp32 tensor on a 2-byte boundary
+    assert f(2, *a, 1, FAKE, FAKE, 1 << 20, None) == 3
+    keep, a = _grad_args(elems=(-4, 4))
+    assert f(2, *a, 1, FAKE, FAKE, 1 << 20, None) == 2
+
+
+def test_clip_refusals(q):
+    f = q.lib.qnf4_clip_grad_norm
+    keep, a = _grad_args()
+    out = (C.c_void_p * 2)(FAKE, FAKE)
+    for bad in (-0.5, float("inf"), float("nan")):
+        assert f(2, *a, 1, bad, C.addressof(out), FAKE, FAKE, 1 << 20, None) == 1
+    assert f(2, *a, 1, 1.0, None, FAKE, FAKE, 1 << 20, None) == 1
+    none = (C.c_void_p * 2)(FAKE, None)
+    assert f(2, *a, 1, 1.0, C.addressof(none), FAKE, FAKE, 1 << 20, None) == 1
+    odd = (C.c_void_p * 2)(FAKE, FAKE + 1)                    # a bf16 output on an odd address
+    assert f(2, *a, 1, 1.0, C.addressof(odd), FAKE, FAKE, 1 << 20, None) == 3
+
+
+def test_grad_workspace_size(q):
+    keep, a = _grad_args(elems=(4096 * 3, 8))
+    # three pieces and one, 8 bytes each, then the factors, both on 256-byte boundaries
+    assert q.lib.qnf4_grad_workspace_size(2, a[2], 1) == 512
+    assert q.lib.qnf4_grad_workspace_size(2, a[2], 0) == 0
+    assert q.lib.qnf4_grad_workspace_size(0, None, 1) == 256
+
+
+def test_binding_refuses_cpu_tensors(q):
+    with pytest.raises(ValueError):
+        q.grad_norm([torch.ones(4)])
+    with pytest.raises(TypeError):
+        q.grad_norm([torch.ones(4, dtype=torch.float64)])
+    with pytest.raises(ValueError):
+        q.clip_grad_norm([torch.ones(4)], 1.0)
