@@ -27,7 +27,8 @@ __all__ = [
     "Nf4Weight", "nf4_codebook", "nf4_quantize", "double_quant", "dequant", "quantize_weight",
     "qlora_linear_fwd", "qlora_linear_bwd", "nf4_recon_error", "rank_topk",
     "dense_linear_fwd", "dense_linear_bwd", "chanq_quantize", "chanq_linear_fwd", "chanq_linear_bwd", "chanq_learn",
-    "grad_norm", "clip_grad_norm", "workspace_size", "check", "set_wait_timeout_ns", "Qnf4Error",
+    "qlora_linear_multi_fwd", "qlora_linear_multi_fwd_group", "qlora_linear_multi_bwd",
+    "dense_linear_multi_fwd", "dense_linear_multi_bwd", "multi_workspace_size", "grad_norm", "clip_grad_norm", "workspace_size", "check", "set_wait_timeout_ns", "Qnf4Error",
 ]
 
 
@@ -448,6 +449,117 @@ def loftq_nf4(W: torch.Tensor, r: int, steps: int = 5, ws=None):
               scale2.data_ptr(), mean.data_ptr(), A.data_ptr(), B.data_ptr(), errs.data_ptr(),
               wsb.data_ptr(), wsb.numel(), _stream(W))
     return Nf4Weight(N, K, packed, code2, scale2, mean[:1]), A, B, errs
+
+
+def multi_workspace_size(op: int, N: int, K: int, M: int, n: int, r: int) -> int:
+    """Workspace bytes of a many-adapter call (op: OP_FWD or OP_BWD)."""
+    return int(lib.qnf4_multi_workspace_size(op, N, K, M, n, r))
+
+
+def _multi_args(N: int, K: int, x, ids, A, B, scales, dY=None):
+    """Checks of a many-adapter call's tensors against one another: (M, n, r)."""
+    for t, nm in ((x, "x"), (A, "A"), (B, "B")):
+        _req(t, torch.bfloat16, nm)
+    _req(ids, torch.int32, "ids")
+    _req(scales, torch.float32, "scales")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [M, {K}], got {tuple(x.shape)}")
+    M = x.shape[0]
+    if A.dim() != 3 or A.shape[2] != K:
+        raise ValueError(f"A must be [n, r, {K}], got {tuple(A.shape)}")
+    n, r = A.shape[0], A.shape[1]
+    if tuple(B.shape) != (n, N, r):
+        raise ValueError(f"B must be [{n}, {N}, {r}], got {tuple(B.shape)}")
+    if tuple(ids.shape) != (M,):
+        raise ValueError(f"ids must be [{M}], got {tuple(ids.shape)}")
+    if tuple(scales.shape) != (n,):
+        raise ValueError(f"scales must be [{n}], got {tuple(scales.shape)}")
+    if dY is not None and tuple(_req(dY, torch.bfloat16, "dY").shape) != (M, N):
+        raise ValueError(f"dY must be [{M}, {N}], got {tuple(dY.shape)}")
+    for t in (ids, A, B, scales) if dY is None else (ids, A, B, scales, dY):
+        if t.device != x.device:
+            raise ValueError("all tensors must be on one device")
+    return M, n, r
+
+
+def _multi_out(t, shape, dtype, name: str, like):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if tuple(_req(t, dtype, name).shape) != tuple(shape) or t.device != like.device:
+        raise ValueError(f"{name} must be {tuple(shape)} on {like.device}")
+    return t
+
+
+def _multi_fwd(fn: str, base, N, K, x, ids, A, B, scales, h, ws):
+    M, n, r = _multi_args(N, K, x, ids, A, B, scales)
+    h = _multi_out(h, (M, N), torch.bfloat16, "h", x)
+    if M == 0:
+        return h
+    with torch.cuda.device(x.device):
+        wsb = _ws(multi_workspace_size(_lib.OP_FWD, N, K, M, n, r), x, ws)
+        _lib.call(fn, *base, x.data_ptr(), M, ids.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
+                  scales.data_ptr(), h.data_ptr(), wsb.data_ptr(), wsb.numel() * wsb.element_size(), _stream(x))
+    return h
+
+
+def _multi_bwd(fn: str, base, N, K, x, dY, ids, A, B, scales, dX, dA, dB, ws):
+    M, n, r = _multi_args(N, K, x, ids, A, B, scales, dY)
+    dX = _multi_out(dX, (M, K), torch.bfloat16, "dX", x)
+    dA = _multi_out(dA, (n, r, K), torch.float32, "dA", x)
+    dB = _multi_out(dB, (n, N, r), torch.float32, "dB", x)
+    if M == 0:
+        dA.zero_()
+        dB.zero_()
+        return dX, dA, dB
+    with torch.cuda.device(x.device):
+        wsb = _ws(multi_workspace_size(_lib.OP_BWD, N, K, M, n, r), x, ws)
+        _lib.call(fn, *base, x.data_ptr(), dY.data_ptr(), M, ids.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
+                  scales.data_ptr(), dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), wsb.data_ptr(),
+                  wsb.numel() * wsb.element_size(), _stream(x))
+    return dX, dA, dB
+
+
+def qlora_linear_multi_fwd(w: Nf4Weight, x: torch.Tensor, ids: torch.Tensor, A: torch.Tensor,
+                           B: torch.Tensor, scales: torch.Tensor, h=None, ws=None) -> torch.Tensor:
+    """The linear layer with n adapters at once over one NF4 base, each token using its own:
+    h[m] = x[m] dequant(W)^T + scales[a] (x[m] A[a]^T) B[a]^T with a = ids[m], bf16 [M, N].
+    ids int32 [M], in any order; an id outside 0 .. n - 1 (e.g. -1) means no adapter. A
+    [n, r, K], B [n, N, r] bf16 (pad an adapter of a lower rank with zero rows of A), scales
+    fp32 [n]."""
+    return _multi_fwd("qnf4_qlora_linear_multi_fwd", (C.byref(w.c()),), w.N, w.K, x, ids, A, B, scales, h, ws)
+
+
+def dense_linear_multi_fwd(W: torch.Tensor, x, ids, A, B, scales, h=None, ws=None) -> torch.Tensor:
+    """``qlora_linear_multi_fwd`` over a 16-bit (protected) base W bf16 [N, K]."""
+    N, K = _req(W, torch.bfloat16, "W").shape
+    return _multi_fwd("qnf4_dense_linear_multi_fwd", (W.data_ptr(), N, K), N, K, x, ids, A, B, scales, h, ws)
+
+
+def qlora_linear_multi_bwd(w: Nf4Weight, x, dY, ids, A, B, scales, dX=None, dA=None, dB=None, ws=None):
+    """Backward of ``qlora_linear_multi_fwd``: (dX bf16 [M, K], dA fp32 [n, r, K], dB fp32
+    [n, N, r]), dA[a] and dB[a] summed over the tokens of adapter a (zeros without any)."""
+    return _multi_bwd("qnf4_qlora_linear_multi_bwd", (C.byref(w.c()),), w.N, w.K, x, dY, ids, A, B, scales,
+                      dX, dA, dB, ws)
+
+
+def dense_linear_multi_bwd(W: torch.Tensor, x, dY, ids, A, B, scales, dX=None, dA=None, dB=None, ws=None):
+    """``qlora_linear_multi_bwd`` over a 16-bit (protected) base W bf16 [N, K]."""
+    N, K = _req(W, torch.bfloat16, "W").shape
+    return _multi_bwd("qnf4_dense_linear_multi_bwd", (W.data_ptr(), N, K), N, K, x, dY, ids, A, B, scales,
+                      dX, dA, dB, ws)
+
+
+def qlora_linear_multi_fwd_group(ws_: list, xs: list, ids: torch.Tensor, As: list, Bs: list,
+                                 scales: torch.Tensor, hs=None, ws=None) -> list:
+    """``qlora_linear_multi_fwd`` of up to 8 independent layers at decode sizes (1..16
+    tokens): every layer has the same tokens, adapters and rank, its own weight, x, A and B."""
+    k = len(ws_)
+    if not 1 <= k <= 8 or not (len(xs) == len(As) == len(Bs) == k):
+        raise ValueError("1 to 8 layers, one x, A and B per layer")
+    if not 1 <= xs[0].shape[0] <= 16:
+        raise ValueError(f"the grouped forward takes 1 to 16 tokens, got {xs[0].shape[0]}")
+    hs = [None] * k if hs is None else hs
+    return [qlora_linear_multi_fwd(w, x, ids, A, B, scales, h, ws) for w, x, A, B, h in zip(ws_, xs, As, Bs, hs)]
 
 
 _GRAD_DTYPES = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}

@@ -69,6 +69,14 @@ SIGNATURES = {
                                    P, P, SZ, P]),
     "qnf4_chanq_learn": (ST, [P, I64, I64, I32, P, I32, P, P, P, P, P]),
     "qnf4_loftq_nf4": (ST, [P, I64, I64, I32, I32, P, P, P, P, P, P, P, P, SZ, P]),
+    "qnf4_multi_workspace_size": (SZ, [I32, I64, I64, I64, I32, I32]),
+    "qnf4_qlora_linear_multi_fwd": (ST, [C.POINTER(Qnf4Weight), P, I64, P, I32, P, P, I32, P, P, P, SZ,
+                                         P]),
+    "qnf4_dense_linear_multi_fwd": (ST, [P, I64, I64, P, I64, P, I32, P, P, I32, P, P, P, SZ, P]),
+    "qnf4_qlora_linear_multi_bwd": (ST, [C.POINTER(Qnf4Weight), P, P, I64, P, I32, P, P, I32, P, P, P,
+                                         P, P, SZ, P]),
+    "qnf4_dense_linear_multi_bwd": (ST, [P, I64, I64, P, P, I64, P, I32, P, P, I32, P, P, P, P, P, SZ,
+                                         P]),
     "qnf4_grad_workspace_size": (SZ, [I32, P, I32]),
     "qnf4_grad_norm": (ST, [I32, P, P, P, I32, P, P, SZ, P]),
     "qnf4_clip_grad_norm": (ST, [I32, P, P, P, I32, F32, P, P, P, SZ, P]),

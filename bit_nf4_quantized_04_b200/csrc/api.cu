@@ -26,6 +26,7 @@
 #include "gemm.cuh"
 #include "grad.cuh"
 #include "loftq.cuh"
+#include "multi.cuh"
 #include "quant.cuh"
 #include "tables.h"
 
@@ -433,20 +434,20 @@ LinPlan plan_linear(int main_src, int64_t N, int64_t K, int64_t M, int r, bool b
   return L;
 }
 
-bool g_smem_set[6][4][3][64] = {};
+bool g_smem_set[2][6][4][3][64] = {};
 
-template <int ASRC, int NSET, int MINB>
+template <int ASRC, int NSET, int MINB, bool MULTI = false>
 qnf4_status launch_gemm(const GemmPlan& p, const CUtensorMap& a, const CUtensorMap& b,
                         const CUtensorMap& bx, const CUtensorMap& o, const CUtensorMap& t, GemmArgs g,
                         cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 64 && !g_smem_set[ASRC][NSET][MINB][dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_gemm<ASRC, NSET, MINB>,
+  if (dev < 64 && !g_smem_set[MULTI][ASRC][NSET][MINB][dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(k_gemm<ASRC, NSET, MINB, MULTI>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmemLimit - 1024));
     if (e != cudaSuccess) return fail(QNF4_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
-    g_smem_set[ASRC][NSET][MINB][dev] = true;
+    g_smem_set[MULTI][ASRC][NSET][MINB][dev] = true;
   }
   if (p.s1 < 1 || p.s1 > kMaxS1 || p.s2 < 0 || p.s2 > kMaxS2 || p.s2 > p.s1 || p.tn < 16 || p.tn > 256 ||
       p.tn % 16 || tmem_cols(ASRC, p.tn, p.s2) > (p.ctas_per_sm == 2 ? 256u : 512u) ||
@@ -482,7 +483,7 @@ qnf4_status launch_gemm(const GemmPlan& p, const CUtensorMap& a, const CUtensorM
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_gemm<ASRC, NSET, MINB>, a, b, bx, o, t, g);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_gemm<ASRC, NSET, MINB, MULTI>, a, b, bx, o, t, g);
   if (e != cudaSuccess) {
     g_launches.fetch_add(1, std::memory_order_relaxed);
     cudaGetLastError();
@@ -521,6 +522,28 @@ qnf4_status launch_any(const GemmPlan& p, const CUtensorMap& a, const CUtensorMa
                                 : launch_gemm<A_DENSE_MN, 1, 1>(p, a, b, bx, o, t, g, s);
     case A_CHANQ_MN: return launch_deq<A_CHANQ_MN>(p, a, b, bx, o, t, g, s);
     default: return launch_deq<A_CHANQ_K>(p, a, b, bx, o, t, g, s);
+  }
+}
+
+// The many-adapter instances: wide tiles and thin ones of each source.
+template <int ASRC>
+qnf4_status launch_multi_src(const GemmPlan& p, const CUtensorMap& a, const CUtensorMap& b,
+                             const CUtensorMap& bx, const CUtensorMap& o, const CUtensorMap& t,
+                             const GemmArgs& g, cudaStream_t s) {
+  constexpr int kWide = src_deq(ASRC) ? kNsetWide : 1;
+  return p.ctas_per_sm == 2 ? launch_gemm<ASRC, 1, 2, true>(p, a, b, bx, o, t, g, s)
+                            : launch_gemm<ASRC, kWide, 1, true>(p, a, b, bx, o, t, g, s);
+}
+
+qnf4_status launch_multi(const GemmPlan& p, const CUtensorMap& a, const CUtensorMap& b,
+                         const CUtensorMap& bx, const CUtensorMap& o, const CUtensorMap& t,
+                         const GemmArgs& g, cudaStream_t s) {
+  switch (p.asrc) {
+    case A_NF4_K: return launch_multi_src<A_NF4_K>(p, a, b, bx, o, t, g, s);
+    case A_NF4_MN: return launch_multi_src<A_NF4_MN>(p, a, b, bx, o, t, g, s);
+    case A_DENSE_K: return launch_multi_src<A_DENSE_K>(p, a, b, bx, o, t, g, s);
+    case A_DENSE_MN: return launch_multi_src<A_DENSE_MN>(p, a, b, bx, o, t, g, s);
+    default: return fail(QNF4_ERR_ARG, "no many-adapter kernel for source %d", p.asrc);
   }
 }
 
@@ -1061,6 +1084,179 @@ LoftqLayout loftq_layout(int64_t N, int64_t K, int r) {
   l.work = o;   o = align256(o + l.lwork * 4);
   l.total = o;
   return l;
+}
+
+// ---------------------------------------------------------------------------
+// Many adapters over one base (see multi.cuh)
+// ---------------------------------------------------------------------------
+constexpr int kMultiMaxAdapters = 4096;
+
+struct MultiPlan {
+  int r16 = 16, per = 4, tn = 16, tiles = 0, dmax = 1, cmax = 1;
+  GemmPlan main;
+  size_t off_cnt = 0, off_list = 0, off_exp = 0, off_pu = 0, off_pv = 0, off_part = 0, off_ctr = 0, total = 0;
+};
+
+MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r, bool bwd, int nsm) {
+  MultiPlan P;
+  P.r16 = ((r + 15) / 16) * 16;
+  P.per = 64 / P.r16;
+  P.tn = tn_for_tokens(M);
+  P.main = bwd ? plan_gemm(main_src, K, M, N, P.tn, 1, nsm) : plan_gemm(main_src, N, M, K, P.tn, 1, nsm);
+  P.tiles = P.main.col_tiles;
+  P.dmax = static_cast<int>(std::min<int64_t>({n, P.tn, M}));
+  P.cmax = (P.dmax + P.per - 1) / P.per;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align256(o + bytes);
+    return at;
+  };
+  P.off_cnt = take(static_cast<size_t>(P.tiles) * sizeof(int));
+  P.off_list = take(static_cast<size_t>(P.tiles) * P.dmax * sizeof(int));
+  P.off_exp = take(static_cast<size_t>(P.tiles) * P.cmax * P.tn * 128);
+  if (bwd) {
+    P.off_pu = take(static_cast<size_t>(M) * P.r16 * sizeof(float));
+    P.off_pv = take(static_cast<size_t>(M) * P.r16 * sizeof(float));
+  }
+  P.off_part = take(P.main.part_floats() * sizeof(float));
+  P.off_ctr = take(static_cast<size_t>(P.main.tiles()) * sizeof(unsigned));
+  P.total = o;
+  return P;
+}
+
+// The adapters of a many-adapter call.
+struct Adapters {
+  const int* ids = nullptr;
+  const void* A = nullptr;
+  const void* B = nullptr;
+  const float* scales = nullptr;
+  int n = 0, r = 0;
+};
+
+// x [M, C] onto its tokens' adapters F (rows j at js, columns at cs, adapters at as elements).
+qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, const void* X, int64_t M, int64_t C,
+                       const void* F, int64_t as, int64_t js, int64_t cs, uint8_t* w8, uint16_t* exp,
+                       float* p32, cudaStream_t s) {
+  launch_pdl(k_multi_proj, dim3(static_cast<unsigned>(M)), dim3(128), 0, s, static_cast<const uint16_t*>(X), C,
+             static_cast<const uint16_t*>(F), as, js, cs, ad.ids, ad.scales, ad.n, ad.r, P.r16, P.tn, P.dmax,
+             P.cmax, reinterpret_cast<const int*>(w8 + P.off_cnt), reinterpret_cast<const int*>(w8 + P.off_list),
+             exp, p32);
+  return launched("multi_proj");
+}
+
+// The base product with the adapters' second product: D = base x X^T + ext (see k_gemm).
+qnf4_status multi_main(const BaseSrc& src, int main_src, const MultiPlan& P, const Adapters& ad, const void* X,
+                       int64_t M, const void* ext, int64_t ext_ld, int64_t ext_as, void* out, uint8_t* w8,
+                       cudaStream_t s) {
+  const int64_t N = src.N, K = src.K;
+  const bool mn = src_mn(main_src);
+  const int64_t rows = mn ? K : N, con = mn ? N : K;
+  CUtensorMap ma, mb, mbx, mo, none;
+  std::memset(&none, 0, sizeof(none));
+  bool ok = true;
+  switch (main_src) {
+    case A_NF4_K: ok = make_map(&ma, src.w->packed, true, K / 2, N, K / 2, 32, 128, false); break;
+    case A_NF4_MN: ok = make_map(&ma, src.w->packed, true, K / 2, N, K / 2, 64, 64, false); break;
+    case A_DENSE_K: ok = make_map(&ma, src.Wd, false, K, N, K, 64, 128, true); break;
+    default: ok = make_map(&ma, src.Wd, false, K, N, K, 64, 64, true); break;
+  }
+  uint16_t* exp = reinterpret_cast<uint16_t*>(w8 + P.off_exp);
+  if (!ok || !make_map(&mb, X, false, con, M, con, 64, P.tn, true) ||
+      !make_map(&mbx, exp, false, 64, static_cast<uint64_t>(P.tiles) * P.cmax * P.tn, 64, 64, P.tn, true))
+    return map_fail();
+  GemmArgs g = base_args();
+  g.ext_k16 = 4;
+  g.ext_r = ad.r;
+  g.ext_a = static_cast<const uint16_t*>(ext);
+  g.ext_ld = ext_ld;
+  g.ext_as = ext_as;
+  g.mt_cnt = reinterpret_cast<const int*>(w8 + P.off_cnt);
+  g.mt_list = reinterpret_cast<const int*>(w8 + P.off_list);
+  g.mt_ids = ad.ids;
+  g.mt_exp = exp;
+  g.mt_n = ad.n;
+  g.mt_dmax = P.dmax;
+  g.mt_cmax = P.cmax;
+  g.mt_per = P.per;
+  g.mt_r16 = P.r16;
+  g.wN = N;
+  g.nbk = K / 64;
+  if (src.w) {
+    g.code2 = src.w->code2;
+    g.scale2 = src.w->scale2;
+    g.mean = src.w->mean;
+    g.packed = src.w->packed;
+    g.cst_elems = N * (K / 64);
+  }
+  g.epi = EPI_BF16;
+  g.out = out;
+  g.o_rs = 1;
+  g.o_cs = rows;
+  g.out_elems = M * rows;
+  g.stage = stage_map(&mo, out, rows, M, rows) ? 1 : 0;
+  g.part = reinterpret_cast<float*>(w8 + P.off_part);
+  g.counters = reinterpret_cast<unsigned*>(w8 + P.off_ctr);
+  if (g_ev_start) cudaEventRecord(g_ev_start, s);
+  const qnf4_status st = launch_multi(P.main, ma, mb, mbx, mo, none, g, s);
+  if (g_ev_stop) cudaEventRecord(g_ev_stop, s);
+  return st;
+}
+
+qnf4_status multi_tiles(const MultiPlan& P, const Adapters& ad, int64_t M, uint8_t* w8, cudaStream_t s) {
+  if (cudaMemsetAsync(w8 + P.off_ctr, 0, P.total - P.off_ctr, s) != cudaSuccess) return launched("memset", 0);
+  launch_pdl(k_multi_tiles, dim3(static_cast<unsigned>(P.tiles)), dim3(256), 0, s, ad.ids, M, ad.n, P.tn, P.dmax,
+             reinterpret_cast<int*>(w8 + P.off_cnt), reinterpret_cast<int*>(w8 + P.off_list));
+  return launched("multi_tiles");
+}
+
+qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int64_t M, void* h, void* ws,
+                      size_t ws_bytes, cudaStream_t s) {
+  const MultiPlan P = plan_multi(src.kind, src.N, src.K, M, ad.n, ad.r, false, num_sms());
+  if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  qnf4_status st = multi_tiles(P, ad, M, w8, s);
+  if (st != QNF4_OK) return st;
+  st = multi_proj(P, ad, x, M, src.K, ad.A, ad.r * src.K, src.K, 1, w8,
+                  reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr, s);
+  if (st != QNF4_OK) return st;
+  return multi_main(src, src.kind, P, ad, x, M, ad.B, ad.r, src.N * ad.r, h, w8, s);
+}
+
+qnf4_status multi_grad(const MultiPlan& P, const Adapters& ad, const void* X, int64_t F, int64_t M, const float* p32,
+                       float* out, int64_t as, int64_t js, int64_t fs, cudaStream_t s) {
+  launch_pdl(k_multi_grad, dim3(static_cast<unsigned>((F + 127) / 128), ad.n, P.r16 / 16), dim3(128), 0, s,
+             static_cast<const uint16_t*>(X), F, M, p32, ad.r, P.r16, ad.ids, out, as, js, fs);
+  return launched("multi_grad");
+}
+
+qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, const void* dY, int64_t M, void* dX,
+                      float* dA, float* dB, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const int64_t N = src.N, K = src.K;
+  const int main_src = src.kind == A_NF4_K ? A_NF4_MN : A_DENSE_MN;
+  const MultiPlan P = plan_multi(main_src, N, K, M, ad.n, ad.r, true, num_sms());
+  if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  float* pu = reinterpret_cast<float*>(w8 + P.off_pu);
+  float* pv = reinterpret_cast<float*>(w8 + P.off_pv);
+  const int r = ad.r;
+  qnf4_status st = multi_tiles(P, ad, M, w8, s);
+  if (st == QNF4_OK)
+    st = multi_proj(P, ad, dY, M, N, ad.B, N * r, 1, r, w8, reinterpret_cast<uint16_t*>(w8 + P.off_exp), pv, s);
+  if (st == QNF4_OK) st = multi_proj(P, ad, x, M, K, ad.A, r * K, K, 1, w8, nullptr, pu, s);
+  if (st == QNF4_OK) st = multi_grad(P, ad, x, K, M, pv, dA, r * K, K, 1, s);
+  if (st == QNF4_OK) st = multi_grad(P, ad, dY, N, M, pu, dB, N * r, 1, r, s);
+  if (st == QNF4_OK) st = multi_main(src, main_src, P, ad, dY, M, ad.A, K, r * K, dX, w8, s);
+  return st;
+}
+
+qnf4_status check_multi_args(int64_t N, int64_t K, int64_t M, int n, int r, bool bwd,
+                             std::initializer_list<const void*> ptrs) {
+  const qnf4_status st = check_linear_args(N, K, M, r, bwd, ptrs);
+  if (st != QNF4_OK) return st;
+  if (n < 1 || n > kMultiMaxAdapters)
+    return fail(QNF4_ERR_ARG, "the number of adapters must be in [1, %d] (got %d)", kMultiMaxAdapters, n);
+  return QNF4_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -1885,6 +2081,94 @@ qnf4_status qnf4_chanq_linear_bwd(const uint8_t* packed, const int64_t* row_off,
     if (st != QNF4_OK) return st;
   }
   return linear_bwd(src, x, dY, M, A, B, r, scale, dX, dA, dB, ws, own, s);
+}
+
+size_t qnf4_multi_workspace_size(int32_t op, int64_t N, int64_t K, int64_t M, int32_t n, int32_t r) {
+  if (N < 1 || K < 1 || M < 1 || n < 1 || r < 1 || r > 64) return 0;
+  // the NF4 and bf16 sources' plans differ in their rings and so in their slices
+  if (op == QNF4_OP_FWD)
+    return std::max(plan_multi(A_NF4_K, N, K, M, n, r, false, num_sms()).total,
+                    plan_multi(A_DENSE_K, N, K, M, n, r, false, num_sms()).total);
+  if (op == QNF4_OP_BWD)
+    return std::max(plan_multi(A_NF4_MN, N, K, M, n, r, true, num_sms()).total,
+                    plan_multi(A_DENSE_MN, N, K, M, n, r, true, num_sms()).total);
+  return 0;
+}
+
+qnf4_status qnf4_qlora_linear_multi_fwd(const qnf4_weight* w, const void* x, int64_t M, const int32_t* ids,
+                                        int32_t n, const void* A, const void* B, int32_t r, const float* scales,
+                                        void* h, void* ws, size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_qlora_linear_multi_fwd");
+  qnf4_status st = check_weight(w);
+  if (st != QNF4_OK) return st;
+  st = check_multi_args(w->N, w->K, M, n, r, false, {x, ids, A, B, scales, h});
+  if (st != QNF4_OK) return st;
+  if (M == 0) return QNF4_OK;
+  BaseSrc src;
+  src.kind = A_NF4_K;
+  src.w = w;
+  src.N = w->N;
+  src.K = w->K;
+  return multi_fwd(src, Adapters{ids, A, B, scales, n, r}, x, M, h, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+qnf4_status qnf4_dense_linear_multi_fwd(const void* W, int64_t N, int64_t K, const void* x, int64_t M,
+                                        const int32_t* ids, int32_t n, const void* A, const void* B, int32_t r,
+                                        const float* scales, void* h, void* ws, size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_dense_linear_multi_fwd");
+  qnf4_status st = check_multi_args(N, K, M, n, r, false, {W, x, ids, A, B, scales, h});
+  if (st != QNF4_OK) return st;
+  if (M == 0) return QNF4_OK;
+  BaseSrc src;
+  src.kind = A_DENSE_K;
+  src.Wd = W;
+  src.N = N;
+  src.K = K;
+  return multi_fwd(src, Adapters{ids, A, B, scales, n, r}, x, M, h, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+qnf4_status qnf4_qlora_linear_multi_bwd(const qnf4_weight* w, const void* x, const void* dY, int64_t M,
+                                        const int32_t* ids, int32_t n, const void* A, const void* B, int32_t r,
+                                        const float* scales, void* dX, float* dA, float* dB, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_qlora_linear_multi_bwd");
+  qnf4_status st = check_weight(w);
+  if (st != QNF4_OK) return st;
+  st = check_multi_args(w->N, w->K, M, n, r, true, {x, dY, ids, A, B, scales, dX, dA, dB});
+  if (st != QNF4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    cudaMemsetAsync(dA, 0, sizeof(float) * n * r * w->K, s);
+    cudaMemsetAsync(dB, 0, sizeof(float) * n * r * w->N, s);
+    return launched("multi_bwd(M=0)", 0);
+  }
+  BaseSrc src;
+  src.kind = A_NF4_K;
+  src.w = w;
+  src.N = w->N;
+  src.K = w->K;
+  return multi_bwd(src, Adapters{ids, A, B, scales, n, r}, x, dY, M, dX, dA, dB, ws, ws_bytes, s);
+}
+
+qnf4_status qnf4_dense_linear_multi_bwd(const void* W, int64_t N, int64_t K, const void* x, const void* dY,
+                                        int64_t M, const int32_t* ids, int32_t n, const void* A, const void* B,
+                                        int32_t r, const float* scales, void* dX, float* dA, float* dB, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_dense_linear_multi_bwd");
+  qnf4_status st = check_multi_args(N, K, M, n, r, true, {W, x, dY, ids, A, B, scales, dX, dA, dB});
+  if (st != QNF4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    cudaMemsetAsync(dA, 0, sizeof(float) * n * r * K, s);
+    cudaMemsetAsync(dB, 0, sizeof(float) * n * r * N, s);
+    return launched("multi_bwd(M=0)", 0);
+  }
+  BaseSrc src;
+  src.kind = A_DENSE_K;
+  src.Wd = W;
+  src.N = N;
+  src.K = K;
+  return multi_bwd(src, Adapters{ids, A, B, scales, n, r}, x, dY, M, dX, dA, dB, ws, ws_bytes, s);
 }
 
 size_t qnf4_grad_workspace_size(int32_t count, const int64_t* elems, int32_t n) {

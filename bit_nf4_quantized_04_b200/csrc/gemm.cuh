@@ -26,6 +26,18 @@
 // TMEM accumulator: the rank-r adapter term of "QLoRA: Efficient Finetuning of
 // Quantized LLMs" (Heng's Blog, opening formula h = dequant(W0) x + (alpha/r) B A x).
 //
+// MULTI instances take many adapters at once (every D column, a token, names its own). The
+// tokens of one column tile name a few distinct adapters, listed per tile beforehand; each
+// adapter is a slot of r16 columns of the extra contraction, 64 / r16 slots to a chunk, and
+// the tile runs as many chunks as its slots fill. Bext is then one tn x 64 block per chunk
+// whose row m holds token m's s u in its own adapter's slot and zeros elsewhere, so the
+// chunks' sum is every token's own term. For the dequantizing sources a chunk is one more
+// step of the A ring (the converters fetch the adapters' rows instead of dequantizing), so
+// chunks run at the pace of ordinary steps; the dense sources write them through the ext
+// tile one at a time. A zero times a non-finite adapter entry would give NaN to the other
+// adapters' tokens: such entries enter the operand as 0 and the epilogue adds their products
+// to their own adapter's tokens alone (ext_fix).
+//
 // Roles (64 + 128 NSET threads): warp 0 issues TMA, warp 1 allocates TMEM and one
 // lane issues tcgen05.mma, and NSET sets of four "converter" warps dequantize (set h
 // takes the steps i with i % NSET == h, one 64-element NF4 block per thread and
@@ -133,6 +145,15 @@ struct GemmArgs {
   const uint8_t* packed;  // A_NF4_K: the packed codes [wN, nbk * 32] (for the L2 prefetch)
   int lut;                // NF4 sources: copies of the shared-memory pair table (16 or 32;
                           // nf4_block_lut), 0 = the register byte planes
+  // many adapters (MULTI): per column tile the number of distinct adapters and their ids in
+  // ascending order; ext_as elements between adapters in ext_a; the tiles' Bext blocks lie
+  // mt_cmax x tn rows apart
+  const int* mt_cnt;      // [column tiles]
+  const int* mt_list;     // [column tiles][mt_dmax]
+  const int* mt_ids;      // [cols] the tokens' adapters
+  const uint16_t* mt_exp; // Bext [column tiles][mt_cmax][tn][64]
+  int64_t ext_as;
+  int mt_n, mt_dmax, mt_cmax, mt_per, mt_r16;
   int lazy_dep;           // programmatic dependent launch: 0 = every thread waits for the
                           // previous grid after the prologue; 1 = only the adapter chunk's
                           // copy waits (its operand is the one the previous grid writes)
@@ -355,8 +376,10 @@ struct Unit {
   int z, splits;       // slice index and slices of this tile (1: a whole tile)
   int pt;              // tail tile index (partials and counter), when splits > 1
   bool ext;            // the adapter chunk is added here (slice 0)
+  int ct, x0, nx;      // MULTI: column tile, first adapter chunk of this slice and their number
 };
 
+template <bool MULTI = false>
 QNF4_DEV Unit unit_of(const GemmArgs& g, int u) {
   Unit w;
   int t;
@@ -381,7 +404,49 @@ QNF4_DEV Unit unit_of(const GemmArgs& g, int u) {
   w.step0 = w.z * sps;
   w.nst = max(0, min(g.nsteps - w.step0, sps));
   w.ext = g.has_ext && w.z == 0;
+  w.ct = t / g.row_tiles;
+  w.x0 = w.nx = 0;
+  if (MULTI) {  // the tile's adapter chunks, dealt to its slices
+    const int chunks = (g.mt_cnt[w.ct] + g.mt_per - 1) / g.mt_per;
+    w.x0 = chunks * w.z / w.splits;
+    w.nx = chunks * (w.z + 1) / w.splits - w.x0;
+  } else {
+    w.nx = w.ext ? 1 : 0;
+  }
   return w;
+}
+
+// bf16 infinities and NaNs: an exponent of all ones. Nonzero where either half of w is one.
+QNF4_DEV uint32_t bf16x2_nonfinite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+// the same word with non-finite halves replaced by zero
+QNF4_DEV uint32_t bf16x2_finite(uint32_t w) {
+  const uint32_t b = bf16x2_nonfinite(w);
+  if (b & 0x8000u) w &= 0xFFFF0000u;
+  if (b & 0x80000000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// What the zeroed non-finite entries of its own adapter add to D[row, col]: their products
+// with the token's s u, in fp32 (the finite entries are in the tensor cores' sum already).
+template <bool MN>
+__device__ __noinline__ float ext_fix(const GemmArgs& g, int64_t row, int64_t col, int ct) {
+  if (row >= g.rows || col >= g.cols) return 0.f;
+  const int a = g.mt_ids[col];
+  const int* list = g.mt_list + static_cast<int64_t>(ct) * g.mt_dmax;
+  int slot = 0;
+  while (slot < g.mt_cnt[ct] && list[slot] != a) ++slot;
+  if (slot == g.mt_cnt[ct]) return 0.f;  // no adapter
+  const int64_t blk = static_cast<int64_t>(ct) * g.mt_cmax + slot / g.mt_per;
+  const uint16_t* u = g.mt_exp + (blk * g.tn + (col - static_cast<int64_t>(ct) * g.tn)) * 64 +
+                      (slot % g.mt_per) * g.mt_r16;
+  const uint16_t* e = g.ext_a + a * g.ext_as;
+  float f = 0.f;
+  for (int j = 0; j < g.ext_r; ++j) {
+    const uint16_t b = MN ? e[j * g.ext_ld + row] : e[row * g.ext_ld + j];
+    if ((b & 0x7F80u) == 0x7F80u)
+      f += __uint_as_float(static_cast<uint32_t>(b) << 16) * __uint_as_float(static_cast<uint32_t>(u[j]) << 16);
+  }
+  return f;
 }
 
 // Where a converter set's step sits in the two rings, advanced without division
@@ -436,23 +501,24 @@ struct ConvCursor {
 // Persistent: CTA b runs units b, b + gridDim.x, ... The load and A rings and their
 // phases continue from unit to unit; the accumulator is handed back and forth
 // through acc_bar (MMAs of a unit done) and acc_empty (its epilogue has read TMEM).
-template <int ASRC, int NSET, int MINB>
+template <int ASRC, int NSET, int MINB, bool MULTI = false>
 __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     k_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
            const __grid_constant__ CUtensorMap tmBx, const __grid_constant__ CUtensorMap tmO,
            const __grid_constant__ CUtensorMap tmT,
-           const GemmArgs g) {
+           const __grid_constant__ GemmArgs g) {
   constexpr bool DEQ = src_deq(ASRC);
   constexpr bool MN = src_mn(ASRC);
   constexpr bool TMA_A = src_tmem_a(ASRC);
   constexpr int NCONV = 128 * NSET;  // converter / epilogue threads
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full1[kMaxS1], empty1[kMaxS1], full2[kMaxS2];
-  __shared__ __align__(8) uint64_t acc_bar, acc_empty, ext_bar, fin_bar;
+  __shared__ __align__(8) uint64_t acc_bar, acc_empty, ext_bar, ext_free, fin_bar;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_last;
   __shared__ float s_lv[16];
+  __shared__ int s_fix[2];  // MULTI, by unit parity: the unit zeroed a non-finite adapter entry
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -474,9 +540,11 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     mbar_init(&acc_bar, 1);
     mbar_init(&acc_empty, NCONV);
     mbar_init(&ext_bar, 128);
+    mbar_init(&ext_free, 1);
     mbar_init(&fin_bar, 1);
     s_abort = 0;
     s_last = 0;
+    s_fix[0] = s_fix[1] = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < 16) s_lv[threadIdx.x] = g.levels[threadIdx.x];
@@ -510,7 +578,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     // per row), so DRAM streams whole row ranges instead of scattered 32-byte pieces.
     if (ASRC == A_NF4_K && g.tn <= 32 && g.packed) {
       for (int u = u0; u < g.nunits; u += ustep) {
-        const Unit w = unit_of(g, u);
+        const Unit w = unit_of<MULTI>(g, u);
         if (w.nst <= 0) continue;
         for (int r = lane; r < kRowsTile; r += 32) {
           const int64_t row = w.row0 + r;
@@ -531,8 +599,8 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       if (src_packed_tma(ASRC)) bytes += kPTile;
       if (src_table_tma(ASRC)) bytes += kTTile;
       for (int u = u0; u < g.nunits && ok; u += ustep) {
-        const Unit w = unit_of(g, u);
-        const int nload = w.nst + (w.ext ? 1 : 0);
+        const Unit w = unit_of<MULTI>(g, u);
+        const int nload = w.nst + w.nx;
         int32_t kc = w.step0 * kStep;
         for (int i = 0; i < nload; ++i) {
           if (!mbar_try_wait(&empty1[s], ph ^ 1) &&
@@ -561,7 +629,8 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
               dep = true;
             }
             mbar_expect_tx(fb, static_cast<uint32_t>(g.tn) * 128u);
-            tma_load_2d(slot + sp.off_b1, &tmBx, fb, 0, (int32_t)w.col0);
+            tma_load_2d(slot + sp.off_b1, &tmBx, fb, 0,
+                        MULTI ? (w.ct * g.mt_cmax + w.x0 + i - w.nst) * g.tn : (int32_t)w.col0);
           }
           ++issued;
           kc += kStep;
@@ -607,7 +676,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       uint32_t ph = 0, ph2 = 0;
       int k = 0, kx = 0;  // units done, adapter chunks done
       for (int u = u0; u < g.nunits; u += ustep, ++k) {
-        const Unit w = unit_of(g, u);
+        const Unit w = unit_of<MULTI>(g, u);
         // the previous unit's epilogue must have read the accumulator
         if (k > 0) {
           if (!wait_or_abort(&acc_empty, (k - 1) & 1, g.wait_ns, &s_abort, 26, true)) {
@@ -616,7 +685,9 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           }
           tc_fence_after();
         }
-        for (int i = 0; i < w.nst; ++i) {
+        // (MULTI, dequantizing sources: the adapter chunks are ordinary steps of the A ring)
+        const int nmma = MULTI && DEQ ? w.nst + w.nx : w.nst;
+        for (int i = 0; i < nmma; ++i) {
           uint64_t* bar = DEQ ? &full2[s2] : &full1[s];
           const uint32_t pp = DEQ ? ph2 : ph;
           if (!mbar_try_wait(bar, pp) && !wait_or_abort(bar, pp, g.wait_ns, &s_abort, DEQ ? 22 : 21)) {
@@ -645,7 +716,32 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           }
         }
         if (!ok) break;
-        if (w.ext) {
+        if (MULTI && !DEQ) {
+          for (int x = 0; x < w.nx; ++x) {
+            if (!wait_or_abort(&full1[s], ph, g.wait_ns, &s_abort, 23) ||
+                !wait_or_abort(&ext_bar, kx & 1, g.wait_ns, &s_abort, 24)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t bd = bdesc0 + static_cast<uint64_t>(static_cast<uint32_t>(s) * b_stride);
+            const uint32_t aa = smem_u32(base + sp.ext);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = MN ? smem_desc(aa + kk * 2048, 8192, 1024, kLayoutSW128)
+                                     : smem_desc(aa + kk * 32, 16, 1024, kLayoutSW128);
+              mma_ss(tmem, ad, bd + 2u * kk, idesc, (w.nst > 0 || x > 0 || kk > 0) ? 1u : 0u);
+            }
+            mma_commit(&empty1[s]);
+            mma_commit(&ext_free);
+            if (++s == S1) {
+              s = 0;
+              ph ^= 1;
+            }
+            ++kx;
+          }
+          if (!ok) break;
+        }
+        if (!MULTI && w.ext) {
           // The adapter chunk: one more position of both rings. Its full2 arrival is
           // bookkeeping only; its B tile and A tile are waited for here.
           if ((DEQ && !wait_or_abort(&full2[s2], ph2, g.wait_ns, &s_abort, 22)) ||
@@ -732,6 +828,74 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       mbar_arrive(&ext_bar);
     };
 
+    // MULTI: row slot `rs` of adapter chunk `chunk` of unit w (the k-th of this CTA), as 64
+    // bf16: D row row0 + rs, one slot of r16 columns per adapter (K-major), or row rs mod 64
+    // of the chunk, one adapter's A row, over the 64 D rows of half rs / 64 (MN-major).
+    // Zero past r, past the slots and past D; non-finite entries are zeroed and flagged.
+    auto ext_words = [&](const Unit& w, int chunk, int rs, int k, uint32_t (&v)[32]) {
+      const int* list = g.mt_list + static_cast<int64_t>(w.ct) * g.mt_dmax;
+      const int nslot = g.mt_cnt[w.ct];
+      const int s0 = chunk * g.mt_per;
+      if (!MN) {
+        const int64_t row = w.row0 + rs;
+        const bool vec = (g.ext_r & 7) == 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int p = 8 * c / g.mt_r16, j0 = 8 * c - p * g.mt_r16;
+          uint4 q4 = make_uint4(0u, 0u, 0u, 0u);
+          if (row < g.rows && p < g.mt_per && s0 + p < nslot && j0 < g.ext_r) {
+            const uint16_t* src = g.ext_a + list[s0 + p] * g.ext_as + row * g.ext_ld + j0;
+            if (vec) {
+              q4 = *reinterpret_cast<const uint4*>(src);
+            } else {
+              uint32_t e[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) e[i] = j0 + i < g.ext_r ? src[i] : 0u;
+              q4 = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
+            }
+          }
+          v[4 * c] = q4.x; v[4 * c + 1] = q4.y; v[4 * c + 2] = q4.z; v[4 * c + 3] = q4.w;
+        }
+      } else {
+        const int kb = rs >> 6, j = rs & 63;
+        const int p = j / g.mt_r16, jj = j - p * g.mt_r16;
+        const int64_t k0 = w.row0 + kb * 64;
+        if (k0 < g.rows && p < g.mt_per && s0 + p < nslot && jj < g.ext_r) {
+          const uint4* src = reinterpret_cast<const uint4*>(g.ext_a + list[s0 + p] * g.ext_as + jj * g.ext_ld + k0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = src[c];
+            v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = 0u;
+        }
+      }
+      uint32_t bad = 0u;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) bad |= bf16x2_nonfinite(v[c]);
+      if (bad) {
+        s_fix[k & 1] = 1;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = bf16x2_finite(v[c]);
+      }
+    };
+    // MULTI, dense sources: the chunks of unit w through the ext tile, one at a time (each
+    // waits until the MMAs of the one before, counted over all units, have read it;
+    // converter set 0 only).
+    int kw = 0;
+    auto write_ext_multi = [&](const Unit& w, int k) {
+      for (int x = 0; x < w.nx; ++x, ++kw) {
+        if (kw > 0 && !wait_or_abort(&ext_free, (kw - 1) & 1, g.wait_ns, &s_abort, 36)) return;
+        uint32_t v[32];
+        ext_words(w, w.x0 + x, t, k, v);
+        store_row_sw128(base + sp.ext, t, v);
+        fence_proxy_async();
+        mbar_arrive(&ext_bar);
+      }
+    };
+
     // Epilogue of the k-th unit of this CTA. Every converter thread calls it for the
     // same units in the same order; it returns false for all of them alike once the
     // CTA has aborted, so all take the same path through the named barriers.
@@ -741,10 +905,12 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       if (ct == 0) s_last = s_abort ? 0 : 2;
       named_sync(1, NCONV);
       const bool have = s_last == 2;
+      const bool fix = MULTI && s_fix[k & 1] != 0;
       named_sync(1, NCONV);
+      if (MULTI && fix && ct == 0) s_fix[k & 1] = 0;  // for unit k + 2
       if (!have) return false;
       tc_fence_after();
-      const Unit w = unit_of(g, u);
+      const Unit w = unit_of<MULTI>(g, u);
       const int64_t row = w.row0 + lrow;
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
       // the sets split the tile's columns in 16-column chunks
@@ -764,6 +930,11 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = r[j];
           if (p + NSET < npiece) tmem_ld8(taddr + (p + NSET) * 8, r);  // next piece in flight
+          if (MULTI && fix) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = __float_as_uint(__uint_as_float(v[j]) + ext_fix<MN>(g, row, w.col0 + p * 8 + j, w.ct));
+          }
           uint16_t* dst = reinterpret_cast<uint16_t*>(stg + b * 2048) + lrow;
 #pragma unroll
           for (int j = 0; j < 8; ++j) dst[j * 128] = f2bf(__uint_as_float(v[j]));
@@ -790,6 +961,10 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+          if (MULTI && fix) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += ext_fix<MN>(g, row, w.col0 + c0 + j, w.ct);
+          }
           epi_store(g, row, w.col0 + c0, v, 16);
         }
         tc_fence_before();
@@ -804,6 +979,11 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           uint32_t r[16];
           tmem_ld16(taddr + c0, r);
           tmem_wait_ld();
+          if (MULTI && fix) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r[j] = __float_as_uint(__uint_as_float(r[j]) + ext_fix<MN>(g, row, w.col0 + c0 + j, w.ct));
+          }
           if (part_ok) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) __stcg(mine + (c0 + j) * 128 + lrow, __uint_as_float(r[j]));
@@ -892,7 +1072,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     auto prefetch_unit = [&](int un) {
       vnext = false;
       if (un < g.nunits) {
-        const Unit wn = unit_of(g, un);
+        const Unit wn = unit_of<MULTI>(g, un);
         bnext = first_block(wn);
         vnext = rowok && set < wn.nst && (ASRC == A_NF4_K || cn < g.wN);
       }
@@ -1067,6 +1247,14 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       }
       return true;
     };
+    // MULTI, dequantizing sources: the step of one adapter chunk.
+    auto ext_step = [&](const Unit& w, const ConvCursor& cur, int k) -> bool {
+      uint32_t o[32];
+      ext_words(w, w.x0 + cur.i - w.nst, slot, k, o);
+      if (!acquire(cur, 37)) return false;
+      publish(cur, o);
+      return true;
+    };
     // per-unit state of the per-channel source: this row's bits, codes and mapping
     auto unit_rows = [&](const Unit& w) {
       if constexpr (ASRC == A_CHANQ_K) {
@@ -1099,16 +1287,16 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       // (dense sources have no A ring: the cursor gets a dummy depth)
       ConvCursor cur(set, rbase, S1, DEQ ? S2 : 1);
       if (live) {
-        const Unit w = unit_of(g, u);
+        const Unit w = unit_of<MULTI>(g, u);
         unit_rows(w);
         if constexpr (ASRC == A_NF4_K || ASRC == A_NF4_MN || ASRC == A_CHANQ_MN) {
           if (set >= w.nst) prefetch_unit(u + ustep);  // no step of this set here
         }
         // positions converted before the previous unit's epilogue
         if (DEQ && up >= 0 && !dead) {
-          const int pre = min(ahead, w.nst + (w.ext ? 1 : 0));
+          const int pre = min(ahead, w.nst + w.nx);
           for (; cur.i < pre; cur.next(NSET, S1, S2)) {
-            if (!(cur.i < w.nst ? step(w, cur, u) : pass_ext(cur))) {
+            if (!(cur.i < w.nst ? step(w, cur, u) : (MULTI ? ext_step(w, cur, k) : pass_ext(cur)))) {
               dead = true;
               break;
             }
@@ -1121,9 +1309,10 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
         if (!more) break;
       }
       if (!live) break;
-      const Unit w = unit_of(g, u);  // recomputed: not kept live across the epilogue
-      const int nload = w.nst + (w.ext ? 1 : 0);
-      if (w.ext && set == 0) write_ext(w);
+      const Unit w = unit_of<MULTI>(g, u);  // recomputed: not kept live across the epilogue
+      const int nload = w.nst + w.nx;
+      if (!MULTI && w.ext && set == 0) write_ext(w);
+      if (MULTI && !DEQ && set == 0 && !dead) write_ext_multi(w, k);
       if (DEQ && !dead) {
         for (; cur.i < w.nst; cur.next(NSET, S1, S2)) {
           if (!step(w, cur, u)) {
@@ -1132,7 +1321,15 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           }
         }
         // the adapter position, when it falls to this set
-        if (!dead && cur.i == w.nst && w.ext && !pass_ext(cur)) dead = true;
+        if (!MULTI && !dead && cur.i == w.nst && w.ext && !pass_ext(cur)) dead = true;
+        if (MULTI && !dead) {
+          for (; cur.i < w.nst + w.nx; cur.next(NSET, S1, S2)) {
+            if (!ext_step(w, cur, k)) {
+              dead = true;
+              break;
+            }
+          }
+        }
       }
       up = u;
       rbase += nload;

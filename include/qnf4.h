@@ -353,6 +353,46 @@ QNF4_API qnf4_status qnf4_loftq_nf4(const void* W_bf16, int64_t N, int64_t K, in
                            float* mean, float* A, float* B, double* errs, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* [QLoRA opening formula, for the adapters of many requests at once] The linear layer with
+ * n (1..4096) adapters over one frozen base, each token using its own:
+ *   h[m] = x[m] bf16(W_hat)^T + scales[a] (x[m] A[a]^T) B[a]^T,   a = ids[m],
+ * h [M, N] bf16, fp32 accumulation, one rounding. ids int32 [M] in any order; an id outside
+ * 0 .. n - 1 (e.g. -1) means no adapter, the base product alone. A [n, r, K] and B [n, N, r]
+ * bf16 (adapters of a lower rank are padded with zero rows of A), scales fp32 [n], all on the
+ * device. An adapter that holds infinities or NaNs reaches its own tokens only. Other
+ * arguments, checks and limits as in qnf4_qlora_linear_fwd; M = 0 is a no-op. Workspace:
+ * qnf4_multi_workspace_size(QNF4_OP_FWD, N, K, M, n, r). */
+QNF4_API size_t qnf4_multi_workspace_size(int32_t op, int64_t N, int64_t K, int64_t M, int32_t n,
+                                 int32_t r);
+QNF4_API qnf4_status qnf4_qlora_linear_multi_fwd(const qnf4_weight* w, const void* x, int64_t M,
+                                        const int32_t* ids, int32_t n, const void* A,
+                                        const void* B, int32_t r, const float* scales, void* h,
+                                        void* ws, size_t ws_bytes, void* stream);
+QNF4_API qnf4_status qnf4_dense_linear_multi_fwd(const void* W_bf16, int64_t N, int64_t K,
+                                        const void* x, int64_t M, const int32_t* ids, int32_t n,
+                                        const void* A, const void* B, int32_t r,
+                                        const float* scales, void* h, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* Its backward, given dY [M, N] bf16: per token (a = ids[m], v[m] = scales[a] dY[m] B[a],
+ * u[m] = scales[a] x[m] A[a]^T, both 0 without an adapter)
+ *   dX[m] = dY[m] bf16(W_hat) + v[m] A[a]      bf16 [M, K]
+ *   dA[a] = sum of v[m]^T x[m]                 fp32 [n, r, K]  over the tokens of adapter a
+ *   dB[a] = sum of dY[m]^T u[m]                fp32 [n, N, r]
+ * dA and dB are written, not accumulated, with zeros for an adapter without tokens (and for
+ * M = 0). N must be a multiple of 8. Workspace: qnf4_multi_workspace_size(QNF4_OP_BWD, ...). */
+QNF4_API qnf4_status qnf4_qlora_linear_multi_bwd(const qnf4_weight* w, const void* x, const void* dY,
+                                        int64_t M, const int32_t* ids, int32_t n, const void* A,
+                                        const void* B, int32_t r, const float* scales, void* dX,
+                                        float* dA, float* dB, void* ws, size_t ws_bytes,
+                                        void* stream);
+QNF4_API qnf4_status qnf4_dense_linear_multi_bwd(const void* W_bf16, int64_t N, int64_t K,
+                                        const void* x, const void* dY, int64_t M,
+                                        const int32_t* ids, int32_t n, const void* A,
+                                        const void* B, int32_t r, const float* scales, void* dX,
+                                        float* dA, float* dB, void* ws, size_t ws_bytes,
+                                        void* stream);
+
 /* [QLoRA opening formula: A and B are all that is trained] The 2-norm of each adapter's
  * gradient over a list of tensors. Tensor t has elems[t] elements (0 is allowed) of dtype[t]
  * (QNF4_OUT_F32 or QNF4_OUT_BF16) and is n equal contiguous parts, part a belonging to

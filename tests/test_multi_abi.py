@@ -71,3 +71,40 @@ def test_binding_refuses_cpu_tensors(q):
         q.grad_norm([torch.ones(4, dtype=torch.float64)])
     with pytest.raises(ValueError):
         q.clip_grad_norm([torch.ones(4)], 1.0)
+
+
+def test_multi_refusals(q):
+    w = q.Qnf4Weight(8, 64, 64, 256, FAKE, FAKE, FAKE, FAKE)
+    big = 1 << 40
+
+    def fwd(w=w, x=FAKE, M=4, ids=FAKE, n=3, A=FAKE, B=FAKE, r=8, s=FAKE, h=FAKE, ws=FAKE, size=big):
+        return q.lib.qnf4_qlora_linear_multi_fwd(C.byref(w), x, M, ids, n, A, B, r, s, h, ws, size, None)
+
+    def bwd(w=w, x=FAKE, dY=FAKE, M=4, ids=FAKE, n=3, A=FAKE, B=FAKE, r=8, s=FAKE, dX=FAKE, dA=FAKE, dB=FAKE,
+            ws=FAKE, size=big):
+        return q.lib.qnf4_qlora_linear_multi_bwd(C.byref(w), x, dY, M, ids, n, A, B, r, s, dX, dA, dB, ws, size, None)
+
+    for f in (fwd, bwd):
+        assert f(n=0) == 1 and f(n=4097) == 1
+        assert f(r=0) == 1 and f(r=65) == 1
+        assert f(M=-1) == 2
+        for arg in ("x", "ids", "A", "B", "s"):
+            assert f(**{arg: None}) == 1 and f(**{arg: FAKE + 8}) == 3
+        assert f(size=16) == 6 and f(ws=None) == 6
+    assert fwd(M=0, ws=None, size=0) == 0
+    assert fwd(h=None) == 1
+    assert bwd(w=q.Qnf4Weight(12, 64, 64, 256, FAKE, FAKE, FAKE, FAKE)) == 2   # N not a multiple of 8
+    assert fwd(w=q.Qnf4Weight(8, 96, 64, 256, FAKE, FAKE, FAKE, FAKE)) == 2
+    d = q.lib.qnf4_dense_linear_multi_fwd
+    assert d(FAKE, 8, 96, FAKE, 4, FAKE, 3, FAKE, FAKE, 8, FAKE, FAKE, FAKE, big, None) == 2
+    assert d(None, 8, 64, FAKE, 4, FAKE, 3, FAKE, FAKE, 8, FAKE, FAKE, FAKE, big, None) == 1
+    d = q.lib.qnf4_dense_linear_multi_bwd
+    assert d(FAKE, 8, 64, FAKE, FAKE, 4, FAKE, 0, FAKE, FAKE, 8, FAKE, FAKE, FAKE, FAKE, FAKE, big, None) == 1
+
+
+def test_multi_workspace_sizes(q):
+    size = q.multi_workspace_size
+    for op in (q._lib.OP_FWD, q._lib.OP_BWD):
+        assert 0 < size(op, 4096, 4096, 1, 1, 1) <= size(op, 4096, 4096, 4096, 1, 16) <= size(op, 4096, 4096, 4096, 64, 16)
+    assert size(q._lib.OP_QUANTIZE, 4096, 4096, 16, 4, 16) == 0
+    assert size(q._lib.OP_FWD, 4096, 4096, 16, 0, 16) == 0
