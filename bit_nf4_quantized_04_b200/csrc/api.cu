@@ -1089,13 +1089,48 @@ LoftqLayout loftq_layout(int64_t N, int64_t K, int r) {
 // ---------------------------------------------------------------------------
 // Many adapters over one base (see multi.cuh)
 // ---------------------------------------------------------------------------
-constexpr int kMultiMaxAdapters = 4096;
+
+// Tiling of the projections: slots per CTA, their batches, contraction slices.
+struct ProjPlan {
+  int sb = 4, nz = 1, slices = 1;
+  uint32_t tmem = 32;
+};
 
 struct MultiPlan {
   int r16 = 16, per = 4, tn = 16, tiles = 0, dmax = 1, cmax = 1;
   GemmPlan main;
-  size_t off_cnt = 0, off_list = 0, off_exp = 0, off_pu = 0, off_pv = 0, off_part = 0, off_ctr = 0, total = 0;
+  ProjPlan proj;
+  // backward: sorted positions, steps per gradient slice, slices, tiles of features
+  int64_t ldp = 0;
+  int lsteps = 1, slmax = 1, ftiles = 0;
+  int64_t part_elems = 0, ctr_elems = 0;
+  size_t off_cnt = 0, off_list = 0, off_exp = 0, off_part = 0, off_ctr = 0;
+  size_t off_pos = 0, off_perm = 0, off_slices = 0, off_nsl = 0, off_bt = 0;
+  size_t off_pt = 0, off_gctr = 0, off_clear_end = 0, off_gpart = 0, total = 0;
 };
+
+constexpr uint32_t kProjRing = 104u * 1024u;  // with 2 CTAs per SM
+constexpr int kProjMaxCols = 128;             // slots x r16 of a batch: two accumulators of 128 columns
+static_assert(3u * (16384u + kProjMaxCols * 128u) <= kProjRing, "three stages");
+static_assert(128u * 65u * 4u + 128u * 64u * 4u <= kProjRing, "the sums reuse the ring");
+
+// About two CTAs per SM: first by slices of the contraction (at least four steps each), then,
+// where few tokens name many adapters, by taking the batches of slots in parallel and making
+// them smaller. With 1024 tokens and more the token tiles fill the SMs, and a tile rarely
+// names more adapters than one batch holds, so its CTAs take the batches one after another.
+ProjPlan plan_proj(int64_t M, int64_t csteps, int jobs, int dmax, int per, int r16, int nsm) {
+  ProjPlan p;
+  const int64_t tiles = (M + 127) / 128 * jobs;
+  const int slots = (dmax + per - 1) / per * per;
+  const int sbmax = kProjMaxCols / r16 / per * per;
+  p.sb = std::min(slots, sbmax);
+  while (p.slices < 8 && tiles * p.slices < 2 * nsm && csteps / (2 * p.slices) >= 4) p.slices *= 2;
+  auto batches = [&] { return (slots + p.sb - 1) / p.sb; };
+  while (p.sb > per && tiles * p.slices * batches() < nsm) p.sb = std::max(per, p.sb / 2 / per * per);
+  p.nz = static_cast<int>(std::min<int64_t>(batches(), std::max<int64_t>(1, 2 * nsm / (tiles * p.slices))));
+  while (p.tmem < static_cast<uint32_t>(2 * p.sb * r16)) p.tmem <<= 1;
+  return p;
+}
 
 MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r, bool bwd, int nsm) {
   MultiPlan P;
@@ -1106,6 +1141,7 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
   P.tiles = P.main.col_tiles;
   P.dmax = static_cast<int>(std::min<int64_t>({n, P.tn, M}));
   P.cmax = (P.dmax + P.per - 1) / P.per;
+  P.proj = plan_proj(M, (bwd ? std::min(N, K) : K) / 64, bwd ? 2 : 1, P.dmax, P.per, P.r16, nsm);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1115,12 +1151,27 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
   P.off_cnt = take(static_cast<size_t>(P.tiles) * sizeof(int));
   P.off_list = take(static_cast<size_t>(P.tiles) * P.dmax * sizeof(int));
   P.off_exp = take(static_cast<size_t>(P.tiles) * P.cmax * P.tn * 128);
-  if (bwd) {
-    P.off_pu = take(static_cast<size_t>(M) * P.r16 * sizeof(float));
-    P.off_pv = take(static_cast<size_t>(M) * P.r16 * sizeof(float));
-  }
   P.off_part = take(P.main.part_floats() * sizeof(float));
   P.off_ctr = take(static_cast<size_t>(P.main.tiles()) * sizeof(unsigned));
+  if (bwd) {
+    P.ldp = (M + 63) / 64 * 64 + 64 * std::min<int64_t>(n, M);
+    P.ftiles = static_cast<int>((K + 127) / 128 + (N + 127) / 128);
+    // slices of 4 to 32 steps: about two CTAs per SM
+    P.lsteps = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(32, M * P.ftiles / (64 * 2 * nsm))));
+    const int64_t several = M / (64 * P.lsteps);  // adapters of more than one slice, at most
+    P.slmax = static_cast<int>(several + n);
+    P.part_elems = 2 * several * P.ftiles * 128 * P.r16;
+    P.ctr_elems = several * P.ftiles;
+    P.off_pos = take(static_cast<size_t>(M) * sizeof(int));
+    P.off_perm = take(static_cast<size_t>(P.ldp) * sizeof(int));
+    P.off_slices = take(static_cast<size_t>(P.slmax) * sizeof(GradSlice));
+    P.off_nsl = take(sizeof(int));
+    P.off_bt = take(static_cast<size_t>(n) * r * N * 2);
+    P.off_pt = take(static_cast<size_t>(6) * P.r16 * P.ldp * 2);
+    P.off_gctr = take(static_cast<size_t>(P.ctr_elems) * sizeof(unsigned));
+    P.off_clear_end = o;
+    P.off_gpart = take(static_cast<size_t>(P.part_elems) * sizeof(float));
+  }
   P.total = o;
   return P;
 }
@@ -1134,14 +1185,87 @@ struct Adapters {
   int n = 0, r = 0;
 };
 
-// x [M, C] onto its tokens' adapters F (rows j at js, columns at cs, adapters at as elements).
-qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, const void* X, int64_t M, int64_t C,
-                       const void* F, int64_t as, int64_t js, int64_t cs, uint8_t* w8, uint16_t* exp,
-                       float* p32, cudaStream_t s) {
-  launch_pdl(k_multi_proj, dim3(static_cast<unsigned>(M)), dim3(128), 0, s, static_cast<const uint16_t*>(X), C,
-             static_cast<const uint16_t*>(F), as, js, cs, ad.ids, ad.scales, ad.n, ad.r, P.r16, P.tn, P.dmax,
-             P.cmax, reinterpret_cast<const int*>(w8 + P.off_cnt), reinterpret_cast<const int*>(w8 + P.off_list),
-             exp, p32);
+bool g_proj_smem_set[64] = {}, g_grad_smem_set[64] = {};
+
+// Launch as launch_pdl does, in clusters of `cluster` CTAs along x, with the kernel's dynamic
+// shared memory limit set once per device.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_multi_kernel(void (*kern)(KArgs...), bool* set, dim3 grid, int threads, size_t smem,
+                                int cluster, cudaStream_t s, const Args&... args) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess && g_launch_err == cudaSuccess) g_launch_err = e;
+  return e;
+}
+
+// One projection of a launch: X [M, C] onto F [n r, C], with the outputs wanted.
+struct ProjJob {
+  const void* X;
+  const void* F;
+  int64_t C;
+  uint16_t* exp;
+  uint16_t* pt;
+};
+
+qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const ProjJob* jobs, int njobs,
+                       uint8_t* w8, cudaStream_t s) {
+  static thread_local ProjArgs g;
+  std::memset(&g, 0, sizeof(g));
+  for (int i = 0; i < njobs; ++i) {
+    const ProjJob& j = jobs[i];
+    if (!make_map(&g.tmX[i], j.X, false, j.C, M, j.C, 64, 128, true) ||
+        !make_map(&g.tmF[i], j.F, false, j.C, static_cast<uint64_t>(ad.n) * ad.r, j.C, 64, P.r16, true))
+      return map_fail();
+    g.nsteps[i] = static_cast<int>((j.C + 63) / 64);
+    g.exp[i] = j.exp;
+    g.pt[i] = j.pt;
+  }
+  g.ids = ad.ids;
+  g.scales = ad.scales;
+  g.pos = reinterpret_cast<const int*>(w8 + P.off_pos);
+  g.M = M;
+  g.ldp = P.ldp;
+  g.n = ad.n;
+  g.r = ad.r;
+  g.r16 = P.r16;
+  g.per = P.per;
+  g.tn = P.tn;
+  g.dmax = P.dmax;
+  g.cmax = P.cmax;
+  g.sb = P.proj.sb;
+  g.nz = P.proj.nz;
+  g.slices = P.proj.slices;
+  g.ring_bytes = kProjRing;
+  g.tmem_cols = P.proj.tmem;
+  g.cnt = reinterpret_cast<int*>(w8 + P.off_cnt);
+  g.list = reinterpret_cast<int*>(w8 + P.off_list);
+  g.ctr = reinterpret_cast<unsigned*>(w8 + P.off_ctr);
+  g.nctr = static_cast<int>(P.main.tiles());
+  g.wait_ns = g_wait_ns;
+  launch_multi_kernel(k_multi_proj, g_proj_smem_set,
+                      dim3(P.proj.slices, static_cast<unsigned>((M + 127) / 128), njobs * P.proj.nz), kMultiThreads,
+                      kProjRing + 1024, P.proj.slices, s, g);
   return launched("multi_proj");
 }
 
@@ -1203,30 +1327,55 @@ qnf4_status multi_main(const BaseSrc& src, int main_src, const MultiPlan& P, con
   return st;
 }
 
-qnf4_status multi_tiles(const MultiPlan& P, const Adapters& ad, int64_t M, uint8_t* w8, cudaStream_t s) {
-  if (cudaMemsetAsync(w8 + P.off_ctr, 0, P.total - P.off_ctr, s) != cudaSuccess) return launched("memset", 0);
-  launch_pdl(k_multi_tiles, dim3(static_cast<unsigned>(P.tiles)), dim3(256), 0, s, ad.ids, M, ad.n, P.tn, P.dmax,
-             reinterpret_cast<int*>(w8 + P.off_cnt), reinterpret_cast<int*>(w8 + P.off_list));
-  return launched("multi_tiles");
-}
-
 qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int64_t M, void* h, void* ws,
                       size_t ws_bytes, cudaStream_t s) {
   const MultiPlan P = plan_multi(src.kind, src.N, src.K, M, ad.n, ad.r, false, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   uint8_t* w8 = static_cast<uint8_t*>(ws);
-  qnf4_status st = multi_tiles(P, ad, M, w8, s);
-  if (st != QNF4_OK) return st;
-  st = multi_proj(P, ad, x, M, src.K, ad.A, ad.r * src.K, src.K, 1, w8,
-                  reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr, s);
+  const ProjJob job{x, ad.A, src.K, reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr};
+  const qnf4_status st = multi_proj(P, ad, M, &job, 1, w8, s);
   if (st != QNF4_OK) return st;
   return multi_main(src, src.kind, P, ad, x, M, ad.B, ad.r, src.N * ad.r, h, w8, s);
 }
 
-qnf4_status multi_grad(const MultiPlan& P, const Adapters& ad, const void* X, int64_t F, int64_t M, const float* p32,
-                       float* out, int64_t as, int64_t js, int64_t fs, cudaStream_t s) {
-  launch_pdl(k_multi_grad, dim3(static_cast<unsigned>((F + 127) / 128), ad.n, P.r16 / 16), dim3(128), 0, s,
-             static_cast<const uint16_t*>(X), F, M, p32, ad.r, P.r16, ad.ids, out, as, js, fs);
+constexpr uint32_t kGradRing = 104u * 1024u;  // with 2 CTAs per SM; at least three stages
+
+qnf4_status multi_grad(const MultiPlan& P, const Adapters& ad, const void* x, const void* dY, int64_t M, int64_t N,
+                       int64_t K, const uint16_t* ptv, const uint16_t* ptu, float* dA, float* dB, uint8_t* w8,
+                       cudaStream_t s) {
+  static thread_local MultiGradArgs g;
+  std::memset(&g, 0, sizeof(g));
+  const int64_t r = ad.r;
+  if (!make_map(&g.tmX[0], x, false, K, M, K, 64, 1, true) || !make_map(&g.tmX[1], dY, false, N, M, N, 64, 1, true) ||
+      !make_map(&g.tmP[0], ptv, false, P.ldp, 3 * P.r16, P.ldp, 64, 3 * P.r16, true) ||
+      !make_map(&g.tmP[1], ptu, false, P.ldp, 3 * P.r16, P.ldp, 64, 3 * P.r16, true))
+    return map_fail();
+  g.out[0] = dA;
+  g.F[0] = K;
+  g.as[0] = r * K;
+  g.js[0] = K;
+  g.fs[0] = 1;
+  g.ft[0] = static_cast<int>((K + 127) / 128);
+  g.out[1] = dB;
+  g.F[1] = N;
+  g.as[1] = N * r;
+  g.js[1] = 1;
+  g.fs[1] = r;
+  g.ft[1] = static_cast<int>((N + 127) / 128);
+  g.r = ad.r;
+  g.r16 = P.r16;
+  g.ring_bytes = kGradRing;
+  g.tmem_cols = 32;
+  while (g.tmem_cols < static_cast<uint32_t>(4 * P.r16)) g.tmem_cols <<= 1;
+  g.slices = reinterpret_cast<const GradSlice*>(w8 + P.off_slices);
+  g.nslices = reinterpret_cast<const int*>(w8 + P.off_nsl);
+  g.perm = reinterpret_cast<const int*>(w8 + P.off_perm);
+  g.part = reinterpret_cast<float*>(w8 + P.off_gpart);
+  g.ctr = reinterpret_cast<unsigned*>(w8 + P.off_gctr);
+  g.part_elems = P.part_elems;
+  g.ctr_elems = P.ctr_elems;
+  g.wait_ns = g_wait_ns;
+  launch_multi_kernel(k_multi_grad, g_grad_smem_set, dim3(P.ftiles, P.slmax), kMultiThreads, kGradRing + 1024, 1, s, g);
   return launched("multi_grad");
 }
 
@@ -1237,17 +1386,39 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   const MultiPlan P = plan_multi(main_src, N, K, M, ad.n, ad.r, true, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   uint8_t* w8 = static_cast<uint8_t*>(ws);
-  float* pu = reinterpret_cast<float*>(w8 + P.off_pu);
-  float* pv = reinterpret_cast<float*>(w8 + P.off_pv);
+  uint16_t* bt = reinterpret_cast<uint16_t*>(w8 + P.off_bt);
+  uint16_t* ptv = reinterpret_cast<uint16_t*>(w8 + P.off_pt);
+  uint16_t* ptu = ptv + 3 * P.r16 * P.ldp;
   const int r = ad.r;
-  qnf4_status st = multi_tiles(P, ad, M, w8, s);
-  if (st == QNF4_OK)
-    st = multi_proj(P, ad, dY, M, N, ad.B, N * r, 1, r, w8, reinterpret_cast<uint16_t*>(w8 + P.off_exp), pv, s);
-  if (st == QNF4_OK) st = multi_proj(P, ad, x, M, K, ad.A, r * K, K, 1, w8, nullptr, pu, s);
-  if (st == QNF4_OK) st = multi_grad(P, ad, x, K, M, pv, dA, r * K, K, 1, s);
-  if (st == QNF4_OK) st = multi_grad(P, ad, dY, N, M, pu, dB, N * r, 1, r, s);
-  if (st == QNF4_OK) st = multi_main(src, main_src, P, ad, dY, M, ad.A, K, r * K, dX, w8, s);
-  return st;
+  PrepArgs pr;
+  std::memset(&pr, 0, sizeof(pr));
+  pr.ids = ad.ids;
+  pr.M = M;
+  pr.n = ad.n;
+  pr.r = r;
+  pr.lsteps = P.lsteps;
+  pr.slmax = P.slmax;
+  pr.ldp = P.ldp;
+  pr.pos = reinterpret_cast<int*>(w8 + P.off_pos);
+  pr.perm = reinterpret_cast<int*>(w8 + P.off_perm);
+  pr.slices = reinterpret_cast<GradSlice*>(w8 + P.off_slices);
+  pr.nslices = reinterpret_cast<int*>(w8 + P.off_nsl);
+  pr.B = static_cast<const uint16_t*>(ad.B);
+  pr.BT = bt;
+  pr.N = N;
+  pr.clear = reinterpret_cast<uint4*>(w8 + P.off_pt);
+  pr.nclear = static_cast<int64_t>(P.off_clear_end - P.off_pt) / 16;
+  const int64_t blocks = std::max<int64_t>(ad.n * ((N + 63) / 64), 8);
+  launch_pdl(k_multi_prep, dim3(1 + static_cast<unsigned>(std::min<int64_t>(blocks, num_sms()))), dim3(kPrepThreads),
+             std::max<size_t>(static_cast<size_t>(ad.n) * (ad.n <= kPrepTable ? 136 : 8), 64u * (r + 1) * 2), s, pr);
+  qnf4_status st = launched("multi_prep");
+  if (st != QNF4_OK) return st;
+  const ProjJob jobs[2] = {{dY, bt, N, reinterpret_cast<uint16_t*>(w8 + P.off_exp), ptv}, {x, ad.A, K, nullptr, ptu}};
+  st = multi_proj(P, ad, M, jobs, 2, w8, s);
+  if (st != QNF4_OK) return st;
+  st = multi_grad(P, ad, x, dY, M, N, K, ptv, ptu, dA, dB, w8, s);
+  if (st != QNF4_OK) return st;
+  return multi_main(src, main_src, P, ad, dY, M, ad.A, K, static_cast<int64_t>(r) * K, dX, w8, s);
 }
 
 qnf4_status check_multi_args(int64_t N, int64_t K, int64_t M, int n, int r, bool bwd,
@@ -1256,6 +1427,7 @@ qnf4_status check_multi_args(int64_t N, int64_t K, int64_t M, int n, int r, bool
   if (st != QNF4_OK) return st;
   if (n < 1 || n > kMultiMaxAdapters)
     return fail(QNF4_ERR_ARG, "the number of adapters must be in [1, %d] (got %d)", kMultiMaxAdapters, n);
+  if (M > 65535 * 128) return fail(QNF4_ERR_SHAPE, "at most %d tokens (got %lld)", 65535 * 128, (long long)M);
   return QNF4_OK;
 }
 

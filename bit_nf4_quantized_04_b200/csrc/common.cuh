@@ -160,6 +160,15 @@ QNF4_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int3
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// Four rows y0 .. y3 of a 2-D tensor (a map whose box is one row high), from column x on.
+QNF4_DEV void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int4 y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z),
+      "r"(y.w)
+      : "memory");
+}
 // Tile shared -> global (bulk async group of the issuing thread; out-of-range
 // elements of the box are not written).
 QNF4_DEV void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
@@ -186,6 +195,27 @@ QNF4_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* ba
           "r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// ----------------------------------------------------------------------------
+// thread-block clusters
+// ----------------------------------------------------------------------------
+QNF4_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Barrier over all threads of the cluster (every CTA of it must come here).
+QNF4_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 at this CTA's shared address `addr` in CTA `rank` of the cluster
+QNF4_DEV float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
 
 // ----------------------------------------------------------------------------

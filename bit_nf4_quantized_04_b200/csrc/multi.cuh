@@ -9,109 +9,764 @@
 // ("QLoRA: Efficient Finetuning of Quantized LLMs" (Heng's Blog), opening formula, for the
 // adapters of many requests or of several trainings at once). The base product and the
 // adapters' second product share one accumulator (the MULTI instances of k_gemm). The
-// kernels here make what those read and the adapters' gradients.
+// kernels here make what those read and the adapters' gradients:
+//
+//   k_multi_prep  (backward) tokens sorted by adapter, B transposed
+//   k_multi_proj  u = s x A^T and v = s dY B of every token's own adapter
+//   k_multi_grad  dA and dB, over the sorted tokens
 #pragma once
 #include "common.cuh"
+#include "gemm.cuh"
 
 namespace qnf4 {
 
-// The distinct adapters of each tile of tn tokens: list[tile][0 .. cnt) ascending.
-__global__ void __launch_bounds__(256) k_multi_tiles(const int* __restrict__ ids, int64_t M, int n, int tn,
-                                                     int dmax, int* __restrict__ cnt, int* __restrict__ list) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ int s_id[256];
-  __shared__ int s_first[256];
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * tn;
-  const int i = threadIdx.x;
-  int id = -1;
-  if (i < tn && m0 + i < M) {
-    id = ids[m0 + i];
-    if (static_cast<unsigned>(id) >= static_cast<unsigned>(n)) id = -1;
-  }
-  s_id[i] = id;
-  __syncthreads();
-  bool first = id >= 0;
-  for (int p = 0; p < i && first; ++p) first = s_id[p] != id;
-  s_first[i] = first;
-  const int total = __syncthreads_count(first);
-  if (first) {
-    int rank = 0;
-    for (int p = 0; p < 256; ++p) rank += s_first[p] && s_id[p] < id;
-    if (in_bounds(rank < dmax, 91)) list[blockIdx.x * static_cast<int64_t>(dmax) + rank] = id;
-  }
-  if (i == 0) cnt[blockIdx.x] = total;
-}
+constexpr int kMultiMaxAdapters = 4096;
+constexpr int kMultiThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr int kMultiMaxStages = 8;
 
-// A token's projection onto its adapter: p[m][j] = scale[a] sum_c X[m, c] F[a as + j js + c cs],
-// written into the tile's blocks of the adapter product (bf16; zeros in the other slots) and,
-// where p32 is given, as fp32 [M][r16]. One CTA per token.
-__global__ void __launch_bounds__(128) k_multi_proj(const uint16_t* __restrict__ X, int64_t C,
-                                                    const uint16_t* __restrict__ F, int64_t as, int64_t js,
-                                                    int64_t cs, const int* __restrict__ ids,
-                                                    const float* __restrict__ scales, int n, int r, int r16,
-                                                    int tn, int dmax, int cmax, const int* __restrict__ cnt,
-                                                    const int* __restrict__ list, uint16_t* __restrict__ exp,
-                                                    float* __restrict__ p32) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float s_p[64];
-  const int64_t m = blockIdx.x;
-  const int a = ids[m];
-  const bool live = static_cast<unsigned>(a) < static_cast<unsigned>(n);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j = warp; j < r16; j += 4) {
-    float v = 0.f;
-    if (live && j < r) {
-      for (int64_t c = lane; c < C; c += 32)
-        v = fmaf(__uint_as_float(static_cast<uint32_t>(X[m * C + c]) << 16),
-                 __uint_as_float(static_cast<uint32_t>(F[a * as + j * js + c * cs]) << 16), v);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      v *= scales[a];
-    }
-    if (lane == 0) {
-      s_p[j] = v;
-      if (p32) p32[m * r16 + j] = v;
+// Wait for a phase regardless of the abort flag, within the drain's limit.
+QNF4_DEV void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long wait_ns, unsigned int site) {
+  const long long t0 = wait_clock();
+  while (!mbar_try_wait_long(bar, parity)) {
+    if (wait_clock() - t0 > ns_cycles(drain_ns(wait_ns))) {
+      set_err(site);
+      return;
     }
   }
-  __syncthreads();
-  if (!exp) return;
-  const int64_t t = m / tn;
-  const int per = 64 / r16, slots = cnt[t];
-  int slot = -1;
-  for (int s = 0; s < slots; ++s)
-    if (live && list[t * dmax + s] == a) slot = s;
-  for (int i = threadIdx.x; i < (slots + per - 1) / per * 64; i += 128) {
-    const int c = i / 64, p = (i % 64) / r16, j = (i % 64) % r16;
-    const bool mine = slot >= 0 && p < per && slot == c * per + p;
-    exp[((t * cmax + c) * tn + (m - t * tn)) * 64 + i % 64] =
-        static_cast<uint16_t>(pack_bf16x2(mine ? s_p[j] : 0.f, 0.f));
+}
+// The last copy issued into each of the ring's slots has landed.
+QNF4_DEV void drain_ring(uint64_t* full, int issued, int nst, unsigned long long wait_ns, unsigned int site) {
+  const int slots = issued < nst ? issued : nst;
+  for (int s = 0; s < slots; ++s) {
+    const int j = s + nst * ((issued - 1 - s) / nst);
+    drain_wait(&full[s], static_cast<uint32_t>(j / nst) & 1u, wait_ns, site);
   }
 }
 
-// out[a as + j js + f fs] = sum over the tokens of a of P[m][j] X[m, f]: a thread per feature f,
-// sixteen rows j per block of the z axis.
-__global__ void __launch_bounds__(128) k_multi_grad(const uint16_t* __restrict__ X, int64_t F, int64_t M,
-                                                    const float* __restrict__ P, int r, int r16,
-                                                    const int* __restrict__ ids, float* __restrict__ out,
-                                                    int64_t as, int64_t js, int64_t fs) {
+// ---------------------------------------------------------------------------
+// Projections onto the tokens' own adapters
+// ---------------------------------------------------------------------------
+// P[m][0 .. r) = scales[a] sum_c X[m, c] F[a][0 .. r)[c]. A CTA takes 128 tokens, a batch of the
+// adapters that their column tile of the main product names (its slots) and a slice of the
+// contraction; X and the adapters' rows come by TMA (128-byte swizzle), one MMA of N = slots x
+// r16 multiplies every token with every slot, and the epilogue keeps each token's own slot:
+// with a few slots per tile the extra products cost nothing beside the stream of X, and rows
+// of different tokens or adapters never mix. The slices of a contraction are the CTAs of a
+// cluster: each leaves its tokens' sums in shared memory and adds up a share of the tokens
+// over all of them, in rank order.
+//
+// The tensor cores' additions truncate: a bf16 sum of C products in one accumulator comes out
+// short by 1.1e-9 C relative (measured: 9.1e-6 at C = 8192), which fp32 gradients would show.
+// So two accumulators take turns, kFlushSteps steps each, and the epilogue warps add them up in
+// registers with rounded fp32 additions while the other one fills.
+//
+// Outputs: the main product's operand blocks (bf16 s u, zeros in the other slots), the tile's
+// list of adapters, and for the gradients the values in three bf16 parts that add up to the
+// fp32 value (8 bits each), transposed to [3 r16][sorted token].
+constexpr int kFlushSteps = 4;
+
+struct ProjArgs {
+  CUtensorMap tmX[2], tmF[2];  // X [M, C] in boxes of 128 x 64, F [n r, C] in boxes of r16 x 64
+  int nsteps[2];
+  uint16_t* exp[2];            // operand blocks [tiles][cmax][tn][64], or null
+  uint16_t* pt[2];             // parts [3 r16][ldp], or null
+  const int* ids;
+  const float* scales;
+  const int* pos;              // sorted position of each token
+  int64_t M, ldp;
+  int n, r, r16, per, tn, dmax, cmax;
+  int sb, nz;                  // slots per batch; CTA z takes the batches z, z + nz, ...
+  int slices;                  // cluster size
+  uint32_t ring_bytes, tmem_cols;
+  int* cnt;                    // [tiles]
+  int* list;                   // [tiles][dmax]
+  unsigned* ctr;               // the main product's arrival counters, cleared here
+  int nctr;
+  unsigned long long wait_ns;
+};
+
+__global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_constant__ ProjArgs g) {
+  extern __shared__ uint8_t psm_raw[];
+  __shared__ __align__(8) uint64_t full[kMultiMaxStages], empty[kMultiMaxStages], acc_full[2], acc_free[2], fin_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ uint32_t s_mask[kMultiMaxAdapters / 32];
+  __shared__ int s_pre[kMultiMaxAdapters / 32];
+  __shared__ int s_total;
+  __shared__ int s_slot[128], s_ad[16];
+  __shared__ float s_scale[128];
+  uint8_t* base = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = g.slices > 1 ? cluster_rank() : 0u;  // == blockIdx.x
+  const int job = blockIdx.z / g.nz, z = blockIdx.z - job * g.nz;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128;
+  const int64_t tile = row0 / g.tn;
+  const int words = (g.n + 31) >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < kMultiMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_free[i], 128);
+    }
+    mbar_init(&fin_bar, 1);
+    s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&g.tmX[job]);
+    tma_prefetch_desc(&g.tmF[job]);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, g.tmem_cols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  for (int i = tid; i < words; i += kMultiThreads) s_mask[i] = 0u;
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t f = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  const int a = blockIdx.y, j0 = blockIdx.z * 16;
-  float acc[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  for (int64_t m = 0; m < M; ++m) {
-    if (ids[m] != a || f >= F) continue;
-    const float x = __uint_as_float(static_cast<uint32_t>(X[m * F + f]) << 16);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = fmaf(P[m * r16 + j0 + j], x, acc[j]);
+
+  // the adapters of the column tile as a bit set; an adapter's slot is its rank in it
+  const int64_t tok0 = tile * g.tn;
+  const int ntok = static_cast<int>(g.M - tok0 < g.tn ? g.M - tok0 : g.tn);
+  for (int i = tid; i < ntok; i += kMultiThreads) {
+    const uint32_t a = static_cast<uint32_t>(g.ids[tok0 + i]);
+    if (a < static_cast<uint32_t>(g.n)) atomicOr(&s_mask[a >> 5], 1u << (a & 31));
   }
-  if (f < F) {
-    for (int j = 0; j < 16; ++j)
-      if (j0 + j < r) out[a * as + (j0 + j) * js + f * fs] = acc[j];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = tid; i < g.nctr; i += kMultiThreads) g.ctr[i] = 0u;
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      const int c = w0 + lane < words ? __popc(s_mask[w0 + lane]) : 0;
+      int inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (w0 + lane < words) s_pre[w0 + lane] = before + inc - c;
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) s_total = before;
+  }
+  __syncthreads();
+  const int total = s_total;
+  const bool lists = z == 0 && job == 0 && blockIdx.x == 0 && row0 == tok0;
+  if (lists && tid == 0) g.cnt[tile] = total;
+  if (tid < 128) {
+    const int64_t m = row0 + tid;
+    const uint32_t a = m < g.M ? static_cast<uint32_t>(g.ids[m]) : 0xffffffffu;
+    const bool live = a < static_cast<uint32_t>(g.n);
+    s_slot[tid] = live ? s_pre[a >> 5] + __popc(s_mask[a >> 5] & ((1u << (a & 31)) - 1u)) : -1;
+    s_scale[tid] = live ? g.scales[a] : 0.f;
+  }
+
+  // the ring's geometry is that of this CTA's first batch, its largest
+  const int r16 = g.r16;
+  const uint32_t fslot = static_cast<uint32_t>(r16) * 128u;
+  const int nb0 = total - z * g.sb < g.sb ? total - z * g.sb : g.sb;
+  const uint32_t stage = 16384u + static_cast<uint32_t>(nb0 > 0 ? nb0 : 0) * fslot;
+  const int fit = static_cast<int>(g.ring_bytes / stage);
+  const int nst = fit < kMultiMaxStages ? fit : kMultiMaxStages;
+  const int per_slice = (g.nsteps[job] + g.slices - 1) / g.slices;
+  const int k0 = static_cast<int>(rank) * per_slice;
+  const int left = g.nsteps[job] - k0;
+  const int steps = left < 0 ? 0 : (left < per_slice ? left : per_slice);
+  int it = 0, blk = 0;  // steps and accumulator turns of earlier batches
+
+  for (int first = z * g.sb; first < total; first += g.nz * g.sb) {  // alike in the whole cluster
+    const int nb = total - first < g.sb ? total - first : g.sb;
+    for (int w = tid; w < words; w += kMultiThreads) {
+      int s = s_pre[w];
+      for (uint32_t m = s_mask[w]; m; m &= m - 1, ++s) {
+        const int a = w * 32 + __ffs(m) - 1;
+        if (s >= first && s < first + nb) s_ad[s - first] = a;
+        if (lists && first == 0 && in_bounds(s < g.dmax, 91)) g.list[tile * g.dmax + s] = a;
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      if (!s_abort) {
+        int issued = it;
+        bool all = true;
+        for (int i = it; i < it + steps && all; ++i) {
+          const int s = i % nst;
+          // every lane waits, so all of them leave together
+          const bool ok = i < nst || wait_or_abort(&empty[s], static_cast<uint32_t>(i / nst - 1) & 1u, g.wait_ns, &s_abort, 91, true);
+          all = __all_sync(0xffffffffu, ok);
+          if (!all) break;
+          uint8_t* st = base + static_cast<uint32_t>(s) * stage;
+          const int32_t c = (k0 + i - it) * 64;
+          if (lane == 0) {
+            mbar_expect_tx(&full[s], 16384u + static_cast<uint32_t>(nb) * fslot);
+            tma_load_2d(st, &g.tmX[job], &full[s], c, static_cast<int32_t>(row0));
+          }
+          __syncwarp();
+          if (lane < nb) tma_load_2d(st + 16384 + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
+          ++issued;
+        }
+        if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 92);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0 && !s_abort) {
+        const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(nb * r16), 0u, 0u);
+        bool ok = true;
+        int b = blk;
+        for (int i = 0; i < steps && ok; ++i) {
+          const int s = (it + i) % nst, turn = i % kFlushSteps;
+          if (turn == 0 && b >= 2)
+            ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 90);
+          ok = ok && wait_or_abort(&full[s], static_cast<uint32_t>((it + i) / nst) & 1u, g.wait_ns, &s_abort, 93);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(base) + static_cast<uint32_t>(s) * stage;
+          const uint64_t ad = smem_desc(st, 16, 1024, kLayoutSW128);
+          const uint64_t bd = smem_desc(st + 16384, 16, 1024, kLayoutSW128);
+          const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_ss(d, ad + 2u * kk, bd + 2u * kk, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&empty[s]);
+          if (turn == kFlushSteps - 1 || i == steps - 1) {
+            mma_commit(&acc_full[b & 1]);
+            ++b;
+          }
+        }
+        if (!ok) {
+          mma_commit(&fin_bar);
+          drain_wait(&fin_bar, 0, g.wait_ns, 95);
+        }
+      }
+      __syncwarp();
+    } else {
+      // add up each token's own slot, then leave the sums in shared memory (the ring is idle
+      // once the batch's MMAs are done)
+      const int q = warp & 3, row = q * 32 + lane;
+      const int mine = s_slot[row] - first;
+      float sum[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) sum[c] = 0.f;
+      const int turns = (steps + kFlushSteps - 1) / kFlushSteps;
+      bool ok = !s_abort;
+      for (int t = 0; t < turns && ok; ++t) {
+        const int b = blk + t;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], static_cast<uint32_t>(b / 2) & 1u, g.wait_ns, &s_abort, 94));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+        for (int sl = 0; sl < nb; ++sl) {
+          if (!__any_sync(0xffffffffu, mine == sl)) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c * 16 < r16) {
+              uint32_t v[16];
+              tmem_ld16(d + sl * r16 + c * 16, v);
+              tmem_wait_ld();
+              if (mine == sl) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(v[j]);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_free[b & 1]);
+      }
+      if (ok) {
+        float* part = reinterpret_cast<float*>(base) + row * (r16 + 1);
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c < r16) part[c] = sum[c];
+      }
+    }
+    it += steps;
+    blk += (steps + kFlushSteps - 1) / kFlushSteps;
+    __syncthreads();
+    if (g.slices > 1) cluster_sync();
+    // this CTA's share of the tokens, summed over the slices
+    const int share = 128 / g.slices, r0 = static_cast<int>(rank) * share;
+    float* fin = reinterpret_cast<float*>(base + 128 * 65 * 4);
+    const uint32_t part0 = smem_u32(base);
+    for (int i = tid; i < share * r16; i += kMultiThreads) {
+      const int row = r0 + i / r16, j = i % r16;
+      const int mine = s_slot[row] - first;
+      float v = 0.f;
+      if (mine >= 0 && mine < nb && j < g.r) {
+        const uint32_t at = part0 + static_cast<uint32_t>(row * (r16 + 1) + j) * 4u;
+        for (int c = 0; c < g.slices; ++c) v += ld_cluster_f32(at, static_cast<uint32_t>(c));
+        v *= s_scale[row];
+      }
+      fin[i] = v;
+    }
+    __syncthreads();
+    const bool ok = !s_abort;
+    if (ok && g.exp[job]) {
+      const int c0 = first / g.per, nch = (nb + g.per - 1) / g.per;
+      for (int i = tid; i < share * nch * 8; i += kMultiThreads) {
+        const int q8 = i & 7, row = (i >> 3) / nch, c = (i >> 3) - row * nch;
+        const int64_t m = row0 + r0 + row;
+        const int p = 8 * q8 / r16, j = 8 * q8 - p * r16;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (p < g.per && s_slot[r0 + row] - first == c * g.per + p) {
+          const float* f = fin + row * r16 + j;
+          v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                         pack_bf16x2(f[6], f[7]));
+        }
+        if (m < g.M)
+          *reinterpret_cast<uint4*>(g.exp[job] + (((tile * g.cmax + c0 + c) * g.tn + (m - tok0)) * 64 + 8 * q8)) = v;
+      }
+    }
+    if (ok && g.pt[job]) {
+      for (int i = tid; i < share * r16; i += kMultiThreads) {
+        const int j = i / share, row = i - j * share;
+        const int mine = s_slot[r0 + row] - first;
+        if (mine < 0 || mine >= nb) continue;
+        float v = fin[row * r16 + j];
+        int64_t at = j * g.ldp + g.pos[row0 + r0 + row];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint16_t h = f2bf(v);
+          g.pt[job][at] = h;
+          // nothing remains of an infinity or a NaN (the difference would be NaN)
+          v = isfinite(v) ? v - __uint_as_float(static_cast<uint32_t>(h) << 16) : 0.f;
+          if (!isfinite(v)) v = 0.f;
+          at += static_cast<int64_t>(r16) * g.ldp;
+        }
+      }
+    }
+    // the others may still be reading this CTA's sums, and the next batch's copies write there
+    fence_proxy_async();
+    if (g.slices > 1) cluster_sync();
+    __syncthreads();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, g.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward preparation
+// ---------------------------------------------------------------------------
+// CTA 0 sorts the tokens by adapter (stable, so equal calls sum in equal order; every warp
+// takes a run of tokens and, where the table of all warps' positions fits, walks it without a
+// barrier, else the warps take 32 tokens each in turn): adapter a's tokens take the positions off[a] .. off[a] + count, each adapter starting on a multiple of
+// 64, with the adapter's last token repeated up to its end (their projections are zero).
+// It cuts every adapter's 64-token steps into slices of at most `lsteps` (one empty slice for
+// an adapter without tokens), the work list of k_multi_grad. The other CTAs transpose B
+// [n, N, r] into BT [n, r, N], clear the projections' parts and the counters.
+struct GradSlice {
+  int a, p0, steps;
+  int count;   // slices of this adapter
+  int index;   // this one among them
+  int group;   // ordinal among the adapters of more than one slice, for counters
+  int part0;   // first of the adapter's slices among those of such adapters, for partials
+  int pad;
+};
+
+struct PrepArgs {
+  const int* ids;
+  int64_t M;
+  int n, r, lsteps, slmax;
+  int64_t ldp;
+  int* pos;          // [M]
+  int* perm;         // [ldp]
+  GradSlice* slices; // [slmax]
+  int* nslices;      // [1]
+  const uint16_t* B;
+  uint16_t* BT;
+  int64_t N;
+  uint4* clear;      // 16-byte words to clear
+  int64_t nclear;
+};
+
+constexpr int kPrepThreads = 1024;
+constexpr int kPrepTable = 256;  // adapters of the per-warp position table (34 KB)
+
+__global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_constant__ PrepArgs g) {
+  extern __shared__ int prep_sm[];
+  __shared__ int s_warp[4][32];
+  __shared__ int s_sum[4];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x == 0) {
+    int* cnt = prep_sm;           // [n] counts
+    int* off = prep_sm + g.n;     // [n] next position of each adapter
+    for (int a = tid; a < g.n; a += kPrepThreads) cnt[a] = 0;
+    if (tid < 4) s_sum[tid] = 0;
+    __syncthreads();
+    for (int64_t m = tid; m < g.M; m += kPrepThreads) {
+      const uint32_t a = static_cast<uint32_t>(g.ids[m]);
+      if (a < static_cast<uint32_t>(g.n)) atomicAdd(&cnt[a], 1);
+    }
+    __syncthreads();
+    // exclusive sums over the adapters of: 64-token steps, slices, adapters of several
+    // slices, and their slices
+    for (int a0 = 0; a0 < g.n; a0 += kPrepThreads) {
+      const int a = a0 + tid;
+      const int c = a < g.n ? cnt[a] : 0;
+      const int steps = (c + 63) >> 6;
+      const int sl = a < g.n ? (steps ? (steps + g.lsteps - 1) / g.lsteps : 1) : 0;
+      const int own[4] = {steps, sl, sl > 1 ? 1 : 0, sl > 1 ? sl : 0};
+      int inc[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        inc[v] = own[v];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, inc[v], o);
+          if (lane >= o) inc[v] += t;
+        }
+        if (lane == 31) s_warp[v][warp] = inc[v];
+      }
+      __syncthreads();
+      if (warp < 4) {
+        const int own_w = s_warp[warp][lane];
+        int w = own_w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, w, o);
+          if (lane >= o) w += t;
+        }
+        const int before = s_sum[warp];
+        __syncwarp();
+        s_warp[warp][lane] = before + w - own_w;
+        if (lane == 31) s_sum[warp] = before + w;
+      }
+      __syncthreads();
+      int ex[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) ex[v] = s_warp[v][warp] + inc[v] - own[v];
+      if (a < g.n) {
+        off[a] = ex[0] * 64;
+        for (int i = 0; i < sl; ++i) {
+          const int st = steps - i * g.lsteps;
+          if (in_bounds(ex[1] + i < g.slmax, 92))
+            g.slices[ex[1] + i] = GradSlice{a, (ex[0] + i * g.lsteps) * 64, st < g.lsteps ? st : g.lsteps, sl, i,
+                                            ex[2], ex[3], 0};
+        }
+      }
+      __syncthreads();
+    }
+    if (tid == 0) *g.nslices = s_sum[1];
+    if (g.n <= kPrepTable) {
+      // a run of tokens per warp: its counts, then its first position in every adapter
+      int* own = prep_sm + 2 * g.n;  // [32][n]
+      for (int i = tid; i < 32 * g.n; i += kPrepThreads) own[i] = 0;
+      const int64_t run = (((g.M + 31) / 32) + 31) / 32 * 32;
+      const int64_t m0 = warp * run, m1 = m0 + run < g.M ? m0 + run : g.M;
+      __syncthreads();
+      for (int64_t m = m0 + lane; m < m1; m += 32) {
+        const uint32_t id = static_cast<uint32_t>(g.ids[m]);
+        if (id < static_cast<uint32_t>(g.n)) atomicAdd(&own[warp * g.n + id], 1);
+      }
+      __syncthreads();
+      for (int a = tid; a < g.n; a += kPrepThreads) {
+        int p = off[a];
+        for (int w = 0; w < 32; ++w) {
+          const int c = own[w * g.n + a];
+          own[w * g.n + a] = p;
+          p += c;
+        }
+        off[a] = p;
+      }
+      __syncthreads();
+      for (int64_t mb = m0; mb < m1; mb += 32) {
+        const int64_t m = mb + lane;
+        const uint32_t id = m < m1 ? static_cast<uint32_t>(g.ids[m]) : 0xffffffffu;
+        const bool live = id < static_cast<uint32_t>(g.n);
+        const uint32_t same = __match_any_sync(0xffffffffu, live ? static_cast<int>(id) : -1);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        int p = -1;
+        if (live) {
+          p = own[warp * g.n + id] + before;
+          if (in_bounds(p < g.ldp, 93)) g.perm[p] = static_cast<int>(m);
+        }
+        if (m < m1) g.pos[m] = p;
+        __syncwarp();
+        if (live && before == 0) own[warp * g.n + id] += __popc(same);
+        __syncwarp();
+      }
+    } else {
+      for (int64_t m0 = 0; m0 < g.M; m0 += kPrepThreads) {
+        const int64_t m = m0 + tid;
+        const uint32_t id = m < g.M ? static_cast<uint32_t>(g.ids[m]) : 0xffffffffu;
+        const bool live = id < static_cast<uint32_t>(g.n);
+        const uint32_t same = __match_any_sync(0xffffffffu, live ? static_cast<int>(id) : -1);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        const int64_t rest = g.M - m0;
+        const int turns = static_cast<int>(rest < kPrepThreads ? (rest + 31) / 32 : 32);
+        int p = -1;
+        for (int w = 0; w < turns; ++w) {
+          if (w == warp) {
+            if (live) p = off[id] + before;
+            __syncwarp();
+            if (live && before == 0) off[id] += __popc(same);
+          }
+          __syncthreads();
+        }
+        if (live && in_bounds(p < g.ldp, 93)) g.perm[p] = static_cast<int>(m);
+        if (m < g.M) g.pos[m] = p;
+      }
+    }
+    // the rest of each adapter's last step: its last token again
+    __threadfence_block();
+    __syncthreads();
+    for (int a = warp; a < g.n; a += kPrepThreads / 32) {
+      const int c = cnt[a];
+      if (c == 0) continue;
+      const int end = off[a], stop = end - c + ((c + 63) & ~63);
+      const int last = g.perm[end - 1];
+      for (int p = end + lane; p < stop; p += 32)
+        if (in_bounds(p < g.ldp, 94)) g.perm[p] = last;
+    }
+    return;
+  }
+  const int64_t nt = (g.N + 63) / 64;
+  uint16_t* sm = reinterpret_cast<uint16_t*>(prep_sm);  // [64][r + 1]
+  for (int64_t u = blockIdx.x - 1; u < nt * g.n; u += gridDim.x - 1) {
+    const int64_t a = u / nt, n0 = (u - a * nt) * 64;
+    const int rows = static_cast<int>(g.N - n0 < 64 ? g.N - n0 : 64);
+    const uint16_t* src = g.B + (a * g.N + n0) * g.r;
+    for (int i = tid; i < rows * g.r; i += kPrepThreads) sm[(i / g.r) * (g.r + 1) + i % g.r] = src[i];
+    __syncthreads();
+    for (int i = tid; i < 64 * g.r; i += kPrepThreads) {
+      const int j = i >> 6, c = i & 63;
+      if (c < rows) g.BT[(a * g.r + j) * g.N + n0 + c] = sm[c * (g.r + 1) + j];
+    }
+    __syncthreads();
+  }
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - 1) * kPrepThreads + tid; i < g.nclear;
+       i += static_cast<int64_t>(gridDim.x - 1) * kPrepThreads)
+    g.clear[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---------------------------------------------------------------------------
+// The adapters' gradients
+// ---------------------------------------------------------------------------
+// G[a][f][j] = sum over the sorted tokens p of adapter a of X[perm[p], f] P[p][j], with X = x
+// and P = v for dA, X = dY and P = u for dB, both in one launch. A CTA takes 128 features and
+// one slice of one adapter's tokens; 64 tokens a step: the TMA warp gathers their rows (four
+// rows per instruction, one instruction per lane) into an MN-major tile, the three parts of P
+// come as a K-major tile of 3 r16 rows, and three MMAs multiply X with them: the first part
+// into one accumulator, the other two, 2^-8 of it, into a second. As in the projections two
+// pairs of accumulators take turns of kFlushSteps steps and are added up in registers.
+// The work is bound by reading X once (it is often still in L2 from the projections); tokens
+// of other adapters are never read, so neither their number nor their values matter. An
+// adapter of several slices goes through fp32 partial tiles that the last of its CTAs to
+// finish adds up in slice order.
+struct MultiGradArgs {
+  CUtensorMap tmX[2];  // x [M, K], dY [M, N]: boxes of 1 x 64, for gathers
+  CUtensorMap tmP[2];  // parts of v, u: [3 r16][ldp] in boxes of 3 r16 x 64
+  float* out[2];
+  int64_t F[2];
+  int64_t as[2], js[2], fs[2];  // element strides of out for adapter, row j, feature
+  int ft[2];                    // feature tiles
+  int r, r16;
+  uint32_t ring_bytes, tmem_cols;
+  const GradSlice* slices;
+  const int* nslices;
+  const int* perm;
+  float* part;                  // [slices of several][ft tiles][r16][128]
+  unsigned* ctr;                // [groups][ft tiles], zero on entry
+  int64_t part_elems, ctr_elems;
+  unsigned long long wait_ns;
+};
+
+__global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_constant__ MultiGradArgs g) {
+  extern __shared__ uint8_t gsm_raw[];
+  __shared__ __align__(8) uint64_t full[kMultiMaxStages], empty[kMultiMaxStages], acc_full[2], acc_free[2], fin_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ int s_last;
+  uint8_t* base = gsm_raw + ((1024u - (smem_u32(gsm_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int job = static_cast<int>(blockIdx.x) < g.ft[0] ? 0 : 1;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x - (job ? g.ft[0] : 0)) * 128;
+  if (tid == 0) {
+    for (int i = 0; i < kMultiMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_free[i], 128);
+    }
+    mbar_init(&fin_bar, 1);
+    s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&g.tmX[job]);
+    tma_prefetch_desc(&g.tmP[job]);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, g.tmem_cols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.y) < *g.nslices) {
+    const GradSlice sl = g.slices[blockIdx.y];
+    const int r16 = g.r16;
+    const uint32_t stage = 16384u + static_cast<uint32_t>(3 * r16) * 128u;
+    const int fit = static_cast<int>(g.ring_bytes / stage);
+    const int nst = fit < kMultiMaxStages ? fit : kMultiMaxStages;
+    if (warp == 0) {
+      int issued = 0;
+      bool all = true;
+      for (int i = 0; i < sl.steps && all; ++i) {
+        const int s = i % nst;
+        const int4 rows = *reinterpret_cast<const int4*>(g.perm + sl.p0 + i * 64 + (lane & 15) * 4);
+        const bool ok = i < nst || wait_or_abort(&empty[s], static_cast<uint32_t>(i / nst - 1) & 1u, g.wait_ns, &s_abort, 96, true);
+        all = __all_sync(0xffffffffu, ok);
+        if (!all) break;
+        uint8_t* st = base + static_cast<uint32_t>(s) * stage;
+        // features past the last one: their D rows are not stored, so nothing is fetched
+        const bool both = f0 + 64 < g.F[job];
+        if (lane == 0) {
+          mbar_expect_tx(&full[s], both ? stage : stage - 8192u);
+          tma_load_2d(st + 16384, &g.tmP[job], &full[s], sl.p0 + i * 64, 0);
+        }
+        __syncwarp();
+        const int half = lane >> 4;
+        if (half == 0 || both)
+          tma_gather4(st + half * 8192 + (lane & 15) * 512, &g.tmX[job], &full[s],
+                      static_cast<int32_t>(f0) + half * 64, rows);
+        ++issued;
+      }
+      if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 97);
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0) {
+        const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
+        const uint32_t pstep = (static_cast<uint32_t>(r16) * 128u) >> 4;  // descriptor units per part
+        bool ok = true;
+        int b = 0;
+        for (int i = 0; i < sl.steps && ok; ++i) {
+          const int s = i % nst, turn = i % kFlushSteps;
+          if (turn == 0 && b >= 2)
+            ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 89);
+          ok = ok && wait_or_abort(&full[s], static_cast<uint32_t>(i / nst) & 1u, g.wait_ns, &s_abort, 98);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(base) + static_cast<uint32_t>(s) * stage;
+          const uint64_t ad = smem_desc(st, 8192, 1024, kLayoutSW128);
+          const uint64_t bd = smem_desc(st + 16384, 16, 1024, kLayoutSW128);
+          const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t a = ad + (2048u >> 4) * kk;
+            const uint32_t acc = (turn > 0 || kk > 0) ? 1u : 0u;
+            mma_ss(d, a, bd + 2u * kk, idesc, acc);
+            mma_ss(d + r16, a, bd + pstep + 2u * kk, idesc, acc);
+            mma_ss(d + r16, a, bd + 2 * pstep + 2u * kk, idesc, 1u);
+          }
+          mma_commit(&empty[s]);
+          if (turn == kFlushSteps - 1 || i == sl.steps - 1) {
+            mma_commit(&acc_full[b & 1]);
+            ++b;
+          }
+        }
+        if (!ok) {
+          mma_commit(&fin_bar);
+          drain_wait(&fin_bar, 0, g.wait_ns, 100);
+        }
+      }
+      __syncwarp();
+    } else {
+      const int q = warp & 3, row = q * 32 + lane;
+      float sum[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) sum[c] = 0.f;
+      const int turns = (sl.steps + kFlushSteps - 1) / kFlushSteps;
+      bool fine = true;
+      for (int b = 0; b < turns && fine; ++b) {
+        fine = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], static_cast<uint32_t>(b / 2) & 1u, g.wait_ns, &s_abort, 99));
+        if (!fine) break;
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c * 16 < r16) {
+            uint32_t hi[16], lo[16];
+            tmem_ld16(d + c * 16, hi);
+            tmem_ld16(d + r16 + c * 16, lo);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(hi[j]) + __uint_as_float(lo[j]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_free[b & 1]);
+      }
+      named_sync(1, 128);
+      const bool ok = !s_abort;
+      named_sync(1, 128);
+      const int64_t f = f0 + row;
+      float* out = g.out[job] + sl.a * g.as[job] + f * g.fs[job];
+      const int64_t js = g.js[job];
+      const bool in = f < g.F[job];
+      const int64_t tiles = g.ft[0] + g.ft[1];
+      const int64_t tsz = static_cast<int64_t>(r16) * 128;
+      const bool several = sl.count > 1;
+      bool write = ok && !several;
+      if (several) {
+        float* mine = g.part + ((sl.part0 + sl.index) * tiles + blockIdx.x) * tsz + row;
+        if (ok && in_bounds(((sl.part0 + sl.index) * tiles + blockIdx.x + 1) * tsz <= g.part_elems, 95)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c < r16) __stcg(mine + c * 128, sum[c]);
+        }
+        __threadfence();
+        named_sync(1, 128);
+        if (tid == 64) {
+          s_last = 0;
+          const int64_t c = sl.group * tiles + blockIdx.x;
+          if (ok && in_bounds(c < g.ctr_elems, 96))
+            s_last = atomicAdd(g.ctr + c, 1u) == static_cast<unsigned>(sl.count - 1);
+        }
+        named_sync(1, 128);
+        write = s_last != 0;
+        if (write) {
+          __threadfence();
+          const float* all = g.part + (sl.part0 * tiles + blockIdx.x) * tsz + row;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sum[c] = 0.f;
+          for (int k = 0; k < sl.count; ++k) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c < r16) sum[c] += __ldcg(all + k * tiles * tsz + c * 128);
+          }
+        }
+      }
+      if (write && in) {
+        if (js == 1 && (g.r & 3) == 0) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 4)
+            if (c < g.r) *reinterpret_cast<float4*>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c < g.r) out[c * js] = sum[c];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, g.tmem_cols);
   }
 }
 

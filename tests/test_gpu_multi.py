@@ -5,8 +5,8 @@ Bounds, elementwise, with u = 2^-24 and b = 2^-8 (half a step of bf16):
   b |su| |B|^T, the output is rounded once, b |h|, and the sums are fp32: a tensor-core sum
   of C products makes C / 16 additions, each off by at most one step, 2 u, of the running
   sum, which the sum of magnitudes bounds;
-* dX likewise; dA and dB are fp32 sums over tokens of projections held as two bf16 halves,
-  whose remainder is at most b^2 of the value: b^2 sum |P| |X| + 2 u (M / 16 + 64) sum |P| |X|
+* dX likewise; dA and dB are fp32 sums over tokens of projections held as three bf16 parts,
+  whose remainder is at most b^3 of the value: (b^3 + 2 u (M / 16 + 64)) sum |P| |X|
   + 2 u (C / 16 + 64) sum |X| (magnitude of P's own contraction).
 With a nonzero base the weight's own rounding to bf16 joins: b per weight (three roundings of
 b where few tokens take the table lookup), independent from weight to weight, so the whole
@@ -85,7 +85,7 @@ def _check_bwd(q, kind, N, K, M, n, r, mix, seed):
             _within(dX, wX, BF * wX.abs() * 1.01 + BF * 1.01 * mX + U2 * ((N + 64 * n) / 16 + 64) * mX * 2, "dX")
         else:
             assert _norm_off(dX, wX) <= 5 * BF
-        tok = BF * BF + U2 * (M / 16 + 64)
+        tok = BF ** 3 + U2 * (M / 16 + 64)
         _within(dA, wA, tok * pA + U2 * (N / 16 + 64) * cA, "dA")
         _within(dB, wB, tok * pB + U2 * (K / 16 + 64) * cB, "dB")
         for a in range(n):
@@ -300,7 +300,7 @@ def test_a_step_of_several_adapters_forward_backward_clip():
     _, (a0, pa0, ca0), (b0, pb0, cb0) = multi_ref.backward(q.dequant(bases[0]), x, d1, ids, A[0], B[0], s)
     want, mags = [a0, b0, a1, b1], [(pa0, ca0), (pb0, cb0), (pa1, ca1), (pb1, cb1)]
     for g, w, (p, c) in zip(keep, want, mags):
-        _within(g, w, (BF * BF + U2 * (M / 16 + 64)) * p + U2 * (D / 16 + 64) * c, "gradient")
+        _within(g, w, (BF ** 3 + U2 * (M / 16 + 64)) * p + U2 * (D / 16 + 64) * c, "gradient")
     exact = torch.stack([t.double().reshape(n, -1).square().sum(1) for t in keep]).sum(0).sqrt()
     assert bool(((norm.double() - exact).abs() <= 1.01 * 2.0 ** -24 * exact).all())
     for g, k in zip(out, keep):
