@@ -558,8 +558,21 @@ def qlora_linear_multi_fwd_group(ws_: list, xs: list, ids: torch.Tensor, As: lis
         raise ValueError("1 to 8 layers, one x, A and B per layer")
     if not 1 <= xs[0].shape[0] <= 16:
         raise ValueError(f"the grouped forward takes 1 to 16 tokens, got {xs[0].shape[0]}")
-    hs = [None] * k if hs is None else hs
-    return [qlora_linear_multi_fwd(w, x, ids, A, B, scales, h, ws) for w, x, A, B, h in zip(ws_, xs, As, Bs, hs)]
+    M, n, r = _multi_args(ws_[0].N, ws_[0].K, xs[0], ids, As[0], Bs[0], scales)
+    for w, x, A, B in zip(ws_[1:], xs[1:], As[1:], Bs[1:]):
+        if _multi_args(w.N, w.K, x, ids, A, B, scales) != (M, n, r):
+            raise ValueError("every layer takes the same tokens, adapters and rank")
+    if hs is None:
+        hs = [torch.empty((M, w.N), dtype=torch.bfloat16, device=xs[0].device) for w in ws_]
+    else:
+        hs = [_multi_out(h, (M, w.N), torch.bfloat16, "h", xs[0]) for w, h in zip(ws_, hs, strict=True)]
+    ptrs = lambda ts: (C.c_void_p * k)(*[t.data_ptr() for t in ts])  # noqa: E731
+    with torch.cuda.device(xs[0].device):
+        wsb = _ws(sum(multi_workspace_size(_lib.OP_FWD, w.N, w.K, M, n, r) for w in ws_), xs[0], ws)
+        _lib.call("qnf4_qlora_linear_multi_fwd_group", k, (_lib.Qnf4Weight * k)(*[w.c() for w in ws_]), ptrs(xs), M,
+                  ids.data_ptr(), n, ptrs(As), ptrs(Bs), r, scales.data_ptr(), ptrs(hs), wsb.data_ptr(),
+                  wsb.numel() * wsb.element_size(), _stream(xs[0]))
+    return hs
 
 
 _GRAD_DTYPES = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}

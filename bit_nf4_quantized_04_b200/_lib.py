@@ -72,6 +72,8 @@ SIGNATURES = {
     "qnf4_multi_workspace_size": (SZ, [I32, I64, I64, I64, I32, I32]),
     "qnf4_qlora_linear_multi_fwd": (ST, [C.POINTER(Qnf4Weight), P, I64, P, I32, P, P, I32, P, P, P, SZ,
                                          P]),
+    "qnf4_qlora_linear_multi_fwd_group": (ST, [I32, C.POINTER(Qnf4Weight), C.POINTER(P), I64, P, I32,
+                                               C.POINTER(P), C.POINTER(P), I32, P, C.POINTER(P), P, SZ, P]),
     "qnf4_dense_linear_multi_fwd": (ST, [P, I64, I64, P, I64, P, I32, P, P, I32, P, P, P, SZ, P]),
     "qnf4_qlora_linear_multi_bwd": (ST, [C.POINTER(Qnf4Weight), P, P, I64, P, I32, P, P, I32, P, P, P,
                                          P, P, SZ, P]),

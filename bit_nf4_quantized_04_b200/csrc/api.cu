@@ -640,34 +640,42 @@ size_t decode_ws_bytes(int64_t K, int64_t M, int r) {
   return align256(static_cast<size_t>(ks) * r * M * sizeof(float));
 }
 
-bool g_dec_smem_set[2][64] = {};
+bool g_dec_smem_set[2][2][64] = {};
 
-template <int Q>
+template <int Q, bool MULTI>
 cudaError_t launch_decode(const DecodeArgs& a, int P, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 64 && !g_dec_smem_set[Q - 1][dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_nf4_decode<Q>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (dev < 64 && !g_dec_smem_set[MULTI][Q - 1][dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(k_nf4_decode<Q, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kDecSmem));
     if (e != cudaSuccess) return e;
-    g_dec_smem_set[Q - 1][dev] = true;
+    g_dec_smem_set[MULTI][Q - 1][dev] = true;
   }
-  return launch_pdl(k_nf4_decode<Q>, dim3(P), dim3(kDecBlockThreads), kDecSmem, s, a, g_wait_ns);
+  return launch_pdl(k_nf4_decode<Q, MULTI>, dim3(P), dim3(kDecBlockThreads), kDecSmem, s, a, g_wait_ns);
 }
 
 // Decode-size forward of n independent layers in one launch pair (k_lora_u, then
-// k_nf4_decode); the layers share M, r and scale. Arguments are checked by the caller.
+// k_nf4_decode); the layers share M, r and scale, or with ids their many adapters (nad of
+// them, with their scales; As and Bs are then stacks). Arguments are checked by the caller.
 qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int64_t M,
                          const void* const* As, const void* const* Bs, int r, float scale,
-                         void* const* hs, void* ws, size_t ws_bytes, cudaStream_t s) {
+                         void* const* hs, void* ws, size_t ws_bytes, cudaStream_t s,
+                         const int* ids = nullptr, int nad = 0, const float* scales = nullptr) {
+  size_t need = 0;
+  for (int l = 0; l < n; ++l) need += decode_ws_bytes(w[l].K, M, r);
+  if (!ws || ws_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, need);
   static thread_local DecodeArgs a;  // about 10 KB: kept off the stack
   std::memset(&a, 0, sizeof(a));
   a.n = n;
   a.M = static_cast<int>(M);
   a.r = r;
   a.scale = scale;
+  a.ids = ids;
+  a.nad = nad;
+  a.scales = scales;
   std::memcpy(a.levels, nf4_tables().levels, sizeof(a.levels));
-  size_t need = 0;
+  size_t off = 0;
   int64_t units = 0, kmax = 0;
   double total = 0.0;  // work = units x K (bytes per unit are 8 K)
   for (int l = 0; l < n; ++l) {
@@ -687,8 +695,8 @@ qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int
     L.A = static_cast<const uint16_t*>(As[l]);
     L.Bm = static_cast<const uint16_t*>(Bs[l]);
     L.h = static_cast<uint16_t*>(hs[l]);
-    L.upart = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + need);
-    need += decode_ws_bytes(K, M, r);
+    L.upart = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off);
+    off += decode_ws_bytes(K, M, r);
     for (int i = 0; i < kDecMaxRb; ++i) {
       const uint32_t rows = 16u * (i + 1);
       const bool ok = L.w3d ? make_map_wcols(&a.wmap[l][i], w[l].packed, K, N, rows)
@@ -701,7 +709,6 @@ qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int
     total += static_cast<double>(rbs) * static_cast<double>(K);
     kmax = std::max(kmax, K);
   }
-  if (!ws || ws_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, need);
   a.units = units;
   // CTA p takes the units from the first one whose start lies at or past p / P of the
   // total work (units x K), so every CTA streams about the same number of bytes
@@ -722,9 +729,13 @@ qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int
   }
   if (g_ev_start) cudaEventRecord(g_ev_start, s);
   const int ksmax = static_cast<int>((kmax + kDecUChunk - 1) / kDecUChunk);
-  cudaError_t e = launch_pdl(k_lora_u, dim3(r, ksmax, n), dim3(128), 0, s, a);
+  cudaError_t e = ids ? launch_pdl(k_lora_u<true>, dim3(r, ksmax, n), dim3(128), 0, s, a)
+                      : launch_pdl(k_lora_u<false>, dim3(r, ksmax, n), dim3(128), 0, s, a);
   if (e != cudaSuccess) return fail(QNF4_ERR_CUDA, "k_lora_u launch: %s", cudaGetErrorString(e));
-  e = M <= 8 ? launch_decode<1>(a, P, s) : launch_decode<2>(a, P, s);
+  if (ids)
+    e = M <= 8 ? launch_decode<1, true>(a, P, s) : launch_decode<2, true>(a, P, s);
+  else
+    e = M <= 8 ? launch_decode<1, false>(a, P, s) : launch_decode<2, false>(a, P, s);
   if (e != cudaSuccess) return fail(QNF4_ERR_CUDA, "k_nf4_decode launch: %s", cudaGetErrorString(e));
   if (g_ev_stop) cudaEventRecord(g_ev_stop, s);
   return launched("decode_fwd", 2);
@@ -2259,8 +2270,9 @@ size_t qnf4_multi_workspace_size(int32_t op, int64_t N, int64_t K, int64_t M, in
   if (N < 1 || K < 1 || M < 1 || n < 1 || r < 1 || r > 64) return 0;
   // the NF4 and bf16 sources' plans differ in their rings and so in their slices
   if (op == QNF4_OP_FWD)
-    return std::max(plan_multi(A_NF4_K, N, K, M, n, r, false, num_sms()).total,
-                    plan_multi(A_DENSE_K, N, K, M, n, r, false, num_sms()).total);
+    return std::max({plan_multi(A_NF4_K, N, K, M, n, r, false, num_sms()).total,
+                     plan_multi(A_DENSE_K, N, K, M, n, r, false, num_sms()).total,
+                     M <= kDecodeMaxTokens ? decode_ws_bytes(K, M, r) : 0});
   if (op == QNF4_OP_BWD)
     return std::max(plan_multi(A_NF4_MN, N, K, M, n, r, true, num_sms()).total,
                     plan_multi(A_DENSE_MN, N, K, M, n, r, true, num_sms()).total);
@@ -2276,12 +2288,34 @@ qnf4_status qnf4_qlora_linear_multi_fwd(const qnf4_weight* w, const void* x, int
   st = check_multi_args(w->N, w->K, M, n, r, false, {x, ids, A, B, scales, h});
   if (st != QNF4_OK) return st;
   if (M == 0) return QNF4_OK;
+  if (M <= kDecodeMaxTokens)
+    return decode_group(1, w, &x, M, &A, &B, r, 0.f, &h, ws, ws_bytes, static_cast<cudaStream_t>(stream), ids, n,
+                        scales);
   BaseSrc src;
   src.kind = A_NF4_K;
   src.w = w;
   src.N = w->N;
   src.K = w->K;
   return multi_fwd(src, Adapters{ids, A, B, scales, n, r}, x, M, h, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+qnf4_status qnf4_qlora_linear_multi_fwd_group(int32_t k, const qnf4_weight* w, const void* const* x, int64_t M,
+                                              const int32_t* ids, int32_t n, const void* const* A,
+                                              const void* const* B, int32_t r, const float* scales,
+                                              void* const* h, void* ws, size_t ws_bytes, void* stream) {
+  TraceRange trace_("qnf4_qlora_linear_multi_fwd_group");
+  if (k < 1 || k > kDecMaxGroup) return fail(QNF4_ERR_ARG, "the layers must be in [1, %d] (got %d)", kDecMaxGroup, k);
+  if (!w || !x || !A || !B || !h) return fail(QNF4_ERR_ARG, "NULL array");
+  if (M < 1 || M > kDecodeMaxTokens)
+    return fail(QNF4_ERR_SHAPE, "the grouped forward takes 1 to %lld tokens (got %lld)",
+                static_cast<long long>(kDecodeMaxTokens), static_cast<long long>(M));
+  for (int l = 0; l < k; ++l) {
+    qnf4_status st = check_weight(&w[l]);
+    if (st != QNF4_OK) return st;
+    st = check_multi_args(w[l].N, w[l].K, M, n, r, false, {x[l], ids, A[l], B[l], scales, h[l]});
+    if (st != QNF4_OK) return st;
+  }
+  return decode_group(k, w, x, M, A, B, r, 0.f, h, ws, ws_bytes, static_cast<cudaStream_t>(stream), ids, n, scales);
 }
 
 qnf4_status qnf4_dense_linear_multi_fwd(const void* W, int64_t N, int64_t K, const void* x, int64_t M,

@@ -53,6 +53,11 @@
 // * Adapter: u = A x^T comes from k_lora_u, launched just before as the primary of a
 //   programmatic dependent launch: the main kernel streams its weights while u is
 //   computed, and waits for it (griddepcontrol.wait) only before its first epilogue.
+// * Many adapters (MULTI): each token names its own (ids), A and B are stacks of n, and the
+//   adapter term leaves the tensor cores: an output row meets up to 16 different B rows, one
+//   per token, so the thread that stores h[m, n] adds s B[a][n] . u[m] in fp32 from the B row
+//   in global memory, which the segment's start asked L2 for. Only the named adapters' rows
+//   are read, and no token meets another's adapter.
 #pragma once
 #include "common.cuh"
 
@@ -119,8 +124,8 @@ struct DecLayer {
   const float* scale2;
   const float* mean;
   const uint16_t* x;         // [M, K] bf16
-  const uint16_t* A;         // [r, K] bf16
-  const uint16_t* Bm;        // [N, r] bf16
+  const uint16_t* A;         // [r, K] bf16 (many adapters: [n, r, K])
+  const uint16_t* Bm;        // [N, r] bf16 (many adapters: [n, N, r])
   float* upart;              // [ks][r][M] fp32
   uint16_t* h;               // [M, N] bf16
 };
@@ -135,6 +140,9 @@ struct DecodeArgs {
   DecLayer L[kDecMaxGroup];
   int n, M, r;
   float scale;
+  const int* ids;       // many adapters: each token's adapter, of nad, and their scales
+  const float* scales;
+  int nad;
   float levels[16];
   int64_t units;                  // 16-row blocks of all layers
   int64_t cta_unit[kDecMaxCta + 1];  // CTA p holds units [cta_unit[p], cta_unit[p + 1])
@@ -176,6 +184,7 @@ QNF4_DEV void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a
 // reduction over its four warps). Launched as a programmatic dependent of whatever ran
 // before: it first waits for that grid, then lets its own dependent (the main kernel)
 // start.
+template <bool MULTI>
 __global__ void __launch_bounds__(128) k_lora_u(const __grid_constant__ DecodeArgs g) {
   griddep_wait();
   griddep_launch_dependents();
@@ -190,14 +199,25 @@ __global__ void __launch_bounds__(128) k_lora_u(const __grid_constant__ DecodeAr
   const bool in = k0 < K;  // K is a multiple of 64, so k0 + 7 < K too
   uint4 av = make_uint4(0u, 0u, 0u, 0u);
   uint4 xv[16];
-  if (in) av = *reinterpret_cast<const uint4*>(L.A + j * K + k0);
+  if (!MULTI && in) av = *reinterpret_cast<const uint4*>(L.A + j * K + k0);
 #pragma unroll
   for (int m = 0; m < 16; ++m)
     xv[m] = (in && m < M) ? *reinterpret_cast<const uint4*>(L.x + m * K + k0) : make_uint4(0u, 0u, 0u, 0u);
-  const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
   float vm[16];
+  uint4 am[MULTI ? 16 : 1];
+  if (MULTI) {  // each token's own adapter row
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+      const int a = m < M ? g.ids[m] : -1;
+      am[m] = in && static_cast<unsigned>(a) < static_cast<unsigned>(g.nad)
+                  ? *reinterpret_cast<const uint4*>(L.A + (static_cast<int64_t>(a) * r + j) * K + k0)
+                  : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
 #pragma unroll
   for (int m = 0; m < 16; ++m) {
+    const uint4 a4 = MULTI ? am[MULTI ? m : 0] : av;
+    const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w};
     const uint32_t xw[4] = {xv[m].x, xv[m].y, xv[m].z, xv[m].w};
     float v = 0.f;
 #pragma unroll
@@ -261,7 +281,7 @@ struct DecRows {
 };
 
 // Q token groups of 8 (Q = 1: M <= 8; Q = 2: M <= 16).
-template <int Q>
+template <int Q, bool MULTI = false>
 __global__ void __launch_bounds__(kDecBlockThreads, 1)
     k_nf4_decode(const __grid_constant__ DecodeArgs g, unsigned long long wait_ns) {
   extern __shared__ uint8_t dsm_raw[];
@@ -423,7 +443,19 @@ __global__ void __launch_bounds__(kDecBlockThreads, 1)
     const bool w3d = L.w3d != 0;
     // this segment's rows of B as bf16 [16R][r16] (zero past r and past N) for the
     // adapter product: 16-byte asynchronous copies when rows are 16-byte aligned
-    if ((r & 7) == 0) {
+    if (MULTI) {
+      // the tokens' own B rows of this segment, 2 r bytes each and contiguous per token
+      for (int m = warp; m < M; m += kDecWarps) {
+        const int a = g.ids[m];
+        const int64_t n1 = row0 + 16 * R < N ? row0 + 16 * R : N;
+        if (static_cast<unsigned>(a) < static_cast<unsigned>(g.nad)) {
+          const uint8_t* b0 = reinterpret_cast<const uint8_t*>(L.Bm + (static_cast<int64_t>(a) * N + row0) * r);
+          const int64_t bytes = (n1 - row0) * r * 2;
+          for (int64_t o = lane * 128; o < bytes; o += 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(b0 + o));
+        }
+      }
+    } else if ((r & 7) == 0) {
       const int pr = r16 / 8;
       for (int i = tid; i < 16 * R * pr; i += kDecThreads) {
         const int rl = i / pr, p = i - pr * (i / pr);
@@ -574,13 +606,19 @@ __global__ void __launch_bounds__(kDecBlockThreads, 1)
               if (c0 + c < L.ks) v += up[c];
           }
         }
-        us[i] = static_cast<uint16_t>(pack_bf16x2(g.scale * v, 0.f) & 0xFFFFu);
+        if (MULTI) {  // fp32, in the B rows' place; zero without an adapter
+          const int a = m < M ? g.ids[m] : -1;
+          reinterpret_cast<float*>(bs)[i] =
+              static_cast<unsigned>(a) < static_cast<unsigned>(g.nad) ? g.scales[a] * v : 0.f;
+        } else {
+          us[i] = static_cast<uint16_t>(pack_bf16x2(g.scale * v, 0.f) & 0xFFFFu);
+        }
       }
       ul = l;
     }
     cp_async_wait_all();  // the B rows
     compute_sync();
-    if (warp == 0) {
+    if (!MULTI && warp == 0) {
       const uint32_t bsa = smem_u32(bs), usa = smem_u32(us);
       for (int kc = 0; kc < r16; kc += 16) {
         uint32_t bu[Q][2];
@@ -634,7 +672,33 @@ __global__ void __launch_bounds__(kDecBlockThreads, 1)
       const int64_t n = row0 + rl;
       if (n >= N) continue;
       const float* p = red + m * kDecRedRow + rl;
-      const float v = ((p[0] + p[16 * kDecRedRow]) + p[2 * 16 * kDecRedRow]) + p[3 * 16 * kDecRedRow];
+      float v = ((p[0] + p[16 * kDecRedRow]) + p[2 * 16 * kDecRedRow]) + p[3 * 16 * kDecRedRow];
+      if (MULTI) {
+        const int a = g.ids[m];
+        if (static_cast<unsigned>(a) < static_cast<unsigned>(g.nad)) {
+          const float* su = reinterpret_cast<const float*>(bs) + m * r16;
+          const uint16_t* b = L.Bm + (static_cast<int64_t>(a) * N + n) * r;
+          float e0 = 0.f, e1 = 0.f;
+          if ((r & 7) == 0) {
+#pragma unroll 4
+            for (int j = 0; j < r; j += 8) {
+              const uint4 q4 = __ldg(reinterpret_cast<const uint4*>(b + j));
+              const float4 s0 = *reinterpret_cast<const float4*>(su + j), s1 = *reinterpret_cast<const float4*>(su + j + 4);
+              e0 = fmaf(bf16lo(q4.x), s0.x, e0);
+              e1 = fmaf(bf16hi(q4.x), s0.y, e1);
+              e0 = fmaf(bf16lo(q4.y), s0.z, e0);
+              e1 = fmaf(bf16hi(q4.y), s0.w, e1);
+              e0 = fmaf(bf16lo(q4.z), s1.x, e0);
+              e1 = fmaf(bf16hi(q4.z), s1.y, e1);
+              e0 = fmaf(bf16lo(q4.w), s1.z, e0);
+              e1 = fmaf(bf16hi(q4.w), s1.w, e1);
+            }
+          } else {
+            for (int j = 0; j < r; ++j) e0 = fmaf(__uint_as_float(static_cast<uint32_t>(__ldg(b + j)) << 16), su[j], e0);
+          }
+          v += e0 + e1;
+        }
+      }
       if (in_bounds(m < M, 74))
         L.h[static_cast<int64_t>(m) * N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
     }

@@ -374,6 +374,17 @@ QNF4_API qnf4_status qnf4_dense_linear_multi_fwd(const void* W_bf16, int64_t N, 
                                         const float* scales, void* h, void* ws, size_t ws_bytes,
                                         void* stream);
 
+/* The forward above for k (1..8) independent layers at decode sizes (1 <= M <= 16) in one
+ * launch pair, bit-identical to k single calls: host arrays w, x, A, B, h of k entries, and
+ * ids, n, r and scales shared by the layers. ws must hold the sum over the layers of
+ * qnf4_multi_workspace_size(QNF4_OP_FWD, N_l, K_l, M, n, r). */
+QNF4_API qnf4_status qnf4_qlora_linear_multi_fwd_group(int32_t k, const qnf4_weight* w,
+                                              const void* const* x, int64_t M,
+                                              const int32_t* ids, int32_t n,
+                                              const void* const* A, const void* const* B,
+                                              int32_t r, const float* scales, void* const* h,
+                                              void* ws, size_t ws_bytes, void* stream);
+
 /* Its backward, given dY [M, N] bf16: per token (a = ids[m], v[m] = scales[a] dY[m] B[a],
  * u[m] = scales[a] x[m] A[a]^T, both 0 without an adapter)
  *   dX[m] = dY[m] bf16(W_hat) + v[m] A[a]      bf16 [M, K]

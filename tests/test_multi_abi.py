@@ -108,3 +108,18 @@ def test_multi_workspace_sizes(q):
         assert 0 < size(op, 4096, 4096, 1, 1, 1) <= size(op, 4096, 4096, 4096, 1, 16) <= size(op, 4096, 4096, 4096, 64, 16)
     assert size(q._lib.OP_QUANTIZE, 4096, 4096, 16, 4, 16) == 0
     assert size(q._lib.OP_FWD, 4096, 4096, 16, 0, 16) == 0
+
+
+def test_multi_group_refusals(q):
+    w = q.Qnf4Weight(8, 64, 64, 256, FAKE, FAKE, FAKE, FAKE)
+    arr = (q.Qnf4Weight * 2)(w, w)
+    p = (C.c_void_p * 2)(FAKE, FAKE)
+
+    def f(k=2, x=p, M=4, ids=FAKE, n=3, A=p, B=p, r=8, s=FAKE, h=p, ws=FAKE, size=1 << 30):
+        return q.lib.qnf4_qlora_linear_multi_fwd_group(k, arr, x, M, ids, n, A, B, r, s, h, ws, size, None)
+
+    assert f(k=0) == 1 and f(k=9) == 1
+    assert f(M=0) == 2 and f(M=17) == 2
+    assert f(x=None) == 1 and f(ids=None) == 1 and f(s=FAKE + 4) == 3 and f(ids=FAKE + 4) == 3
+    assert f(n=0) == 1 and f(r=65) == 1 and f(r=0) == 1
+    assert f(A=(C.c_void_p * 2)(FAKE, None)) == 1
