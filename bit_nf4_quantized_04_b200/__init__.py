@@ -13,7 +13,10 @@ from __future__ import annotations
 
 import ctypes as C
 from array import array
+from contextlib import nullcontext
 from dataclasses import dataclass
+from functools import lru_cache
+from operator import attrgetter, is_ as _IS
 
 import torch
 
@@ -451,6 +454,19 @@ def loftq_nf4(W: torch.Tensor, r: int, steps: int = 5, ws=None):
     return Nf4Weight(N, K, packed, code2, scale2, mean[:1]), A, B, errs
 
 
+_NO_SWITCH = nullcontext()
+
+
+def _on(t: torch.Tensor):
+    """The context of t's device: the library launches on the current one."""
+    return _NO_SWITCH if torch.cuda.current_device() == t.get_device() else torch.cuda.device(t.device)
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+@lru_cache(maxsize=4096)
 def multi_workspace_size(op: int, N: int, K: int, M: int, n: int, r: int) -> int:
     """Workspace bytes of a many-adapter call (op: OP_FWD or OP_BWD)."""
     return int(lib.qnf4_multi_workspace_size(op, N, K, M, n, r))
@@ -476,18 +492,29 @@ def _multi_args(N: int, K: int, x, ids, A, B, scales, dY=None):
         raise ValueError(f"scales must be [{n}], got {tuple(scales.shape)}")
     if dY is not None and tuple(_req(dY, torch.bfloat16, "dY").shape) != (M, N):
         raise ValueError(f"dY must be [{M}, {N}], got {tuple(dY.shape)}")
+    d = x.get_device()
     for t in (ids, A, B, scales) if dY is None else (ids, A, B, scales, dY):
-        if t.device != x.device:
+        if t.get_device() != d:
             raise ValueError("all tensors must be on one device")
     return M, n, r
 
 
 def _multi_out(t, shape, dtype, name: str, like):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(_req(t, dtype, name).shape) != tuple(shape) or t.device != like.device:
+        return like.new_empty(shape, dtype=dtype)
+    if tuple(_req(t, dtype, name).shape) != tuple(shape) or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be {tuple(shape)} on {like.device}")
     return t
+
+
+def _multi_ws(need: int, like: torch.Tensor, ws):
+    """(pointer owner, its bytes) of the caller's workspace, or of a new one."""
+    if ws is None:
+        return like.new_empty(need, dtype=torch.uint8), need
+    _ws(need, like, ws)
+    if ws.get_device() != like.get_device():
+        raise ValueError("the workspace must be on the tensors' device")
+    return ws, ws.numel() * ws.element_size()
 
 
 def _multi_fwd(fn: str, base, N, K, x, ids, A, B, scales, h, ws):
@@ -495,10 +522,10 @@ def _multi_fwd(fn: str, base, N, K, x, ids, A, B, scales, h, ws):
     h = _multi_out(h, (M, N), torch.bfloat16, "h", x)
     if M == 0:
         return h
-    with torch.cuda.device(x.device):
-        wsb = _ws(multi_workspace_size(_lib.OP_FWD, N, K, M, n, r), x, ws)
+    with _on(x):
+        wsb, size = _multi_ws(multi_workspace_size(_lib.OP_FWD, N, K, M, n, r), x, ws)
         _lib.call(fn, *base, x.data_ptr(), M, ids.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
-                  scales.data_ptr(), h.data_ptr(), wsb.data_ptr(), wsb.numel() * wsb.element_size(), _stream(x))
+                  scales.data_ptr(), h.data_ptr(), wsb.data_ptr(), size, _raw_stream(x))
     return h
 
 
@@ -511,11 +538,11 @@ def _multi_bwd(fn: str, base, N, K, x, dY, ids, A, B, scales, dX, dA, dB, ws):
         dA.zero_()
         dB.zero_()
         return dX, dA, dB
-    with torch.cuda.device(x.device):
-        wsb = _ws(multi_workspace_size(_lib.OP_BWD, N, K, M, n, r), x, ws)
+    with _on(x):
+        wsb, size = _multi_ws(multi_workspace_size(_lib.OP_BWD, N, K, M, n, r), x, ws)
         _lib.call(fn, *base, x.data_ptr(), dY.data_ptr(), M, ids.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
-                  scales.data_ptr(), dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), wsb.data_ptr(),
-                  wsb.numel() * wsb.element_size(), _stream(x))
+                  scales.data_ptr(), dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), wsb.data_ptr(), size,
+                  _raw_stream(x))
     return dX, dA, dB
 
 
@@ -563,60 +590,66 @@ def qlora_linear_multi_fwd_group(ws_: list, xs: list, ids: torch.Tensor, As: lis
         if _multi_args(w.N, w.K, x, ids, A, B, scales) != (M, n, r):
             raise ValueError("every layer takes the same tokens, adapters and rank")
     if hs is None:
-        hs = [torch.empty((M, w.N), dtype=torch.bfloat16, device=xs[0].device) for w in ws_]
+        hs = [xs[0].new_empty((M, w.N)) for w in ws_]
     else:
         hs = [_multi_out(h, (M, w.N), torch.bfloat16, "h", xs[0]) for w, h in zip(ws_, hs, strict=True)]
     ptrs = lambda ts: (C.c_void_p * k)(*[t.data_ptr() for t in ts])  # noqa: E731
-    with torch.cuda.device(xs[0].device):
-        wsb = _ws(sum(multi_workspace_size(_lib.OP_FWD, w.N, w.K, M, n, r) for w in ws_), xs[0], ws)
+    with _on(xs[0]):
+        wsb, size = _multi_ws(sum([multi_workspace_size(_lib.OP_FWD, w.N, w.K, M, n, r) for w in ws_]), xs[0], ws)
         _lib.call("qnf4_qlora_linear_multi_fwd_group", k, (_lib.Qnf4Weight * k)(*[w.c() for w in ws_]), ptrs(xs), M,
-                  ids.data_ptr(), n, ptrs(As), ptrs(Bs), r, scales.data_ptr(), ptrs(hs), wsb.data_ptr(),
-                  wsb.numel() * wsb.element_size(), _stream(xs[0]))
+                  ids.data_ptr(), n, ptrs(As), ptrs(Bs), r, scales.data_ptr(), ptrs(hs), wsb.data_ptr(), size,
+                  _raw_stream(xs[0]))
     return hs
 
 
 _GRAD_DTYPES = {torch.float32: _lib.OUT_F32, torch.bfloat16: _lib.OUT_BF16}
 
 
+_dtype_of = attrgetter("dtype")
+_is_contiguous, _get_device = torch.Tensor.is_contiguous, torch.Tensor.get_device
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+
+
 def _grad_list(ts, what: str):
-    """Host arrays (pointers, dtypes, element counts) of a list of gradients."""
-    for t in ts:
-        if t.dtype not in _GRAD_DTYPES:
-            raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{what} must be CUDA tensors")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-    if len({t.device for t in ts}) > 1:
-        raise ValueError(f"{what} must be on one device")
-    return (array("Q", [t.data_ptr() for t in ts]), array("i", [_GRAD_DTYPES[t.dtype] for t in ts]),
-            array("q", [t.numel() for t in ts]))
+    """Host arrays (pointers, dtypes, element counts) of a list of gradients, and its device.
+    One C-level pass per property: the list of a whole model is a thousand tensors."""
+    dts = list(map(_dtype_of, ts))
+    for dt in set(dts):
+        if dt not in _GRAD_DTYPES:
+            raise TypeError(f"{what} must be float32 or bfloat16, got {dt}")
+    devs = set(map(_get_device, ts))
+    if len(devs) != 1 or -1 in devs:
+        raise ValueError(f"{what} must be CUDA tensors on one device")
+    if not all(map(_is_contiguous, ts)):
+        raise ValueError(f"{what} must be contiguous")
+    return (array("Q", list(map(_data_ptr, ts))), array("i", list(map(_GRAD_DTYPES.__getitem__, dts))),
+            array("q", list(map(_numel, ts))), devs.pop())
 
 
 def _grad_call(grads, n: int, norm, ws, max_norm=None, out=None):
-    grads = list(grads)
     if not grads:
         raise ValueError("the list of gradients is empty")
-    ptr, dt, num = _grad_list(grads, "gradients")
-    dev = grads[0].device
+    ptr, dt, num, dev = _grad_list(grads, "gradients")
+    like = grads[0]
     if norm is None:
-        norm = torch.empty(n, dtype=torch.float32, device=dev)
-    elif _req(norm, torch.float32, "norm").numel() != n or norm.device != dev:
-        raise ValueError(f"norm must hold {n} values on {dev}")
+        norm = like.new_empty(n, dtype=torch.float32)
+    elif _req(norm, torch.float32, "norm").numel() != n or norm.get_device() != dev:
+        raise ValueError(f"norm must hold {n} values on the gradients' device")
     a = [v.buffer_info()[0] for v in (ptr, dt, num)]
     args = (len(grads), *a, n)
     if out is not None:
-        optr, odt, onum = _grad_list(out, "outputs")
-        if odt != dt or onum != num or out[0].device != dev:
+        same = len(out) == len(grads) and all(map(_IS, out, grads))
+        optr, odt, onum, odev = (ptr, dt, num, dev) if same else _grad_list(out, "outputs")
+        if odt != dt or onum != num or odev != dev:
             raise ValueError("one output per gradient, of its dtype, size and device")
         live = [p for p, m in zip(optr, num) if m]
         if len(set(live)) != len(live):
             raise ValueError("an output appears twice")
         args += (float(max_norm), optr.buffer_info()[0])
-    with torch.cuda.device(dev):
-        wsb = _ws(int(lib.qnf4_grad_workspace_size(len(grads), a[2], n)), grads[0], ws)
+    with _on(like):
+        wsb, size = _multi_ws(max(int(lib.qnf4_grad_workspace_size(len(grads), a[2], n)), 16), like, ws)
         _lib.call("qnf4_grad_norm" if out is None else "qnf4_clip_grad_norm", *args, norm.data_ptr(),
-                  wsb.data_ptr(), wsb.numel() * wsb.element_size(), _stream(grads[0]))
+                  wsb.data_ptr(), size, _raw_stream(like))
     return norm
 
 
@@ -625,7 +658,7 @@ def grad_norm(grads, n: int = 1, norm=None, ws=None) -> torch.Tensor:
     Each tensor is n equal contiguous parts, part a belonging to adapter a (the layout of dA
     [n, r, K] and dB [n, N, r]); n = 1 gives the global norm. Summed in float64, in a fixed
     order."""
-    return _grad_call(grads, n, norm, ws)
+    return _grad_call(list(grads), n, norm, ws)
 
 
 def clip_grad_norm(grads, max_norm: float, n: int = 1, out=None, norm=None, ws=None):

@@ -1479,7 +1479,8 @@ qnf4_status check_grad_args(int32_t count, const void* const* g, const int32_t* 
 }
 
 // The launches' table of tensors [t0, t0 + count).
-void grad_tab(GradTab* tab, int32_t t0, int32_t count, const void* const* g, const int32_t* dtype,
+template <int CAP>
+void grad_tab(GradTab<CAP>* tab, int32_t t0, int32_t count, const void* const* g, const int32_t* dtype,
               const int64_t* elems, int32_t n, void* const* out, int64_t base, int64_t pieces) {
   std::memset(tab->bf16, 0, sizeof(tab->bf16));
   tab->count = count;
@@ -1497,7 +1498,8 @@ void grad_tab(GradTab* tab, int32_t t0, int32_t count, const void* const* g, con
   }
 }
 
-qnf4_status grad_norm_clip(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+template <int CAP>
+qnf4_status grad_norm_clip_in(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
                            int32_t n, float max_norm, void* const* out, float* norm, void* ws,
                            size_t ws_bytes, cudaStream_t s) {
   if (!ws || !al16(ws) || ws_bytes < grad_ws_bytes(count, elems, n))
@@ -1507,21 +1509,21 @@ qnf4_status grad_norm_clip(int32_t count, const void* const* g, const int32_t* d
   double* sums = static_cast<double*>(ws);
   float* coef = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                          align256(static_cast<size_t>(pieces) * n * sizeof(double)));
-  static thread_local GradTab tab;  // 16 KB: kept off the stack
+  static thread_local GradTab<CAP> tab;  // up to 16 KB: kept off the stack
   int launches = 0;
   auto pass = [&](bool scale) {
     int64_t base = 0;
-    for (int32_t t0 = 0; t0 < count; t0 += kGradMaxTensors) {
-      grad_tab(&tab, t0, std::min(kGradMaxTensors, count - t0), g, dtype, elems, n, out, base, pieces);
+    for (int32_t t0 = 0; t0 < count; t0 += CAP) {
+      grad_tab<CAP>(&tab, t0, std::min(CAP, count - t0), g, dtype, elems, n, out, base, pieces);
       const int64_t per = tab.piece0[tab.count];
       base += per;
       if (per == 0) continue;
       const int64_t ctas = (per * n + kGradWarps - 1) / kGradWarps;
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ctas, num_sms() * 8)));
       if (scale)
-        launch_pdl(k_grad_scale, grid, dim3(32 * kGradWarps), 0, s, tab, static_cast<const float*>(coef));
+        launch_pdl(k_grad_scale<CAP>, grid, dim3(32 * kGradWarps), 0, s, tab, static_cast<const float*>(coef));
       else
-        launch_pdl(k_grad_sq, grid, dim3(32 * kGradWarps), 0, s, tab, sums);
+        launch_pdl(k_grad_sq<CAP>, grid, dim3(32 * kGradWarps), 0, s, tab, sums);
       ++launches;
     }
   };
@@ -1531,6 +1533,14 @@ qnf4_status grad_norm_clip(int32_t count, const void* const* g, const int32_t* d
   ++launches;
   if (out) pass(true);
   return launched(out ? "clip_grad_norm" : "grad_norm", launches);
+}
+
+qnf4_status grad_norm_clip(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                           int32_t n, float max_norm, void* const* out, float* norm, void* ws,
+                           size_t ws_bytes, cudaStream_t s) {
+  return count <= kGradFewTensors
+             ? grad_norm_clip_in<kGradFewTensors>(count, g, dtype, elems, n, max_norm, out, norm, ws, ws_bytes, s)
+             : grad_norm_clip_in<kGradMaxTensors>(count, g, dtype, elems, n, max_norm, out, norm, ws, ws_bytes, s);
 }
 
 }  // namespace

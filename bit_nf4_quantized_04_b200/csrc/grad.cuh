@@ -18,16 +18,20 @@
 
 namespace qnf4 {
 
-constexpr int kGradMaxTensors = 512;  // per launch (the table travels in the kernel's arguments)
+// Tensors per launch: the table travels in the kernel's arguments (32 bytes a tensor), which a
+// short list keeps short.
+constexpr int kGradMaxTensors = 512;
+constexpr int kGradFewTensors = 32;
 constexpr int kGradWarps = 8;
 constexpr int kGradPiece = 4096;      // elements of a piece
 
+template <int CAP>
 struct GradTab {
-  const void* in[kGradMaxTensors];
-  void* out[kGradMaxTensors];
-  int64_t part[kGradMaxTensors];           // elements of one adapter's part
-  int64_t piece0[kGradMaxTensors + 1];     // pieces per adapter before tensor t (in this launch)
-  uint32_t bf16[kGradMaxTensors / 32];     // bit t: tensor t is bf16, else fp32
+  const void* in[CAP];
+  void* out[CAP];
+  int64_t part[CAP];           // elements of one adapter's part
+  int64_t piece0[CAP + 1];     // pieces per adapter before tensor t (in this launch)
+  uint32_t bf16[CAP / 32];     // bit t: tensor t is bf16, else fp32
   int count;                               // tensors in this launch
   int n;                                   // adapters
   int64_t base;                            // pieces per adapter in earlier launches
@@ -39,7 +43,8 @@ struct GradPiece {
   int t;
   int64_t e0, e1;
 };
-QNF4_DEV GradPiece grad_piece(const GradTab& g, int64_t q) {
+template <int CAP>
+QNF4_DEV GradPiece grad_piece(const GradTab<CAP>& g, int64_t q) {
   int lo = 0, hi = g.count - 1;  // last tensor with piece0 <= q (empty tensors hold no piece)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -53,7 +58,8 @@ QNF4_DEV GradPiece grad_piece(const GradTab& g, int64_t q) {
   return p;
 }
 
-QNF4_DEV bool grad_is_bf16(const GradTab& g, int t) { return (g.bf16[t >> 5] >> (t & 31)) & 1u; }
+template <int CAP>
+QNF4_DEV bool grad_is_bf16(const GradTab<CAP>& g, int t) { return (g.bf16[t >> 5] >> (t & 31)) & 1u; }
 QNF4_DEV float bf16_of(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 QNF4_DEV double sq_add(double s, float v) { return fma(static_cast<double>(v), static_cast<double>(v), s); }
 
@@ -65,7 +71,8 @@ QNF4_DEV int64_t head_elems(const T* p, int64_t n) {
 }
 
 // part_sum[a * pieces + q] = the squares of piece q of adapter a
-__global__ void __launch_bounds__(32 * kGradWarps) k_grad_sq(const __grid_constant__ GradTab g,
+template <int CAP>
+__global__ void __launch_bounds__(32 * kGradWarps) k_grad_sq(const __grid_constant__ GradTab<CAP> g,
                                                             double* __restrict__ part_sum) {
   griddep_wait();
   griddep_launch_dependents();
@@ -143,7 +150,8 @@ __global__ void __launch_bounds__(512) k_grad_norm(const double* __restrict__ pa
 }
 
 // out = g * coef[a]; where the output is the input, an adapter whose factor is 1 is left.
-__global__ void __launch_bounds__(32 * kGradWarps) k_grad_scale(const __grid_constant__ GradTab g,
+template <int CAP>
+__global__ void __launch_bounds__(32 * kGradWarps) k_grad_scale(const __grid_constant__ GradTab<CAP> g,
                                                                const float* __restrict__ coef) {
   griddep_wait();
   griddep_launch_dependents();
