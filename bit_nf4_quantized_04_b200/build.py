@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libqnf4.so")
 # an index outside its buffer is skipped and reported by qnf4_check as QNF4_ERR_BOUNDS.
 LIB_CHECKED = os.path.join(HERE, "libqnf4_checked.so")
 SOURCES = ["api.cu", "codebook.cpp"]
-HEADERS = ["common.cuh", "quant.cuh", "chanq.cuh", "gemm.cuh", "decode.cuh", "loftq.cuh", "multi.cuh", "grad.cuh",
+HEADERS = ["common.cuh", "quant.cuh", "chanq.cuh", "gemm.cuh", "decode.cuh", "loftq.cuh", "multi.cuh", "multi_mm.cuh",
+           "grad.cuh",
            "tables.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -27,6 +27,7 @@
 #include "grad.cuh"
 #include "loftq.cuh"
 #include "multi.cuh"
+#include "multi_mm.cuh"
 #include "quant.cuh"
 #include "tables.h"
 
@@ -191,6 +192,21 @@ bool make_map(CUtensorMap* m, const void* ptr, bool u8, uint64_t inner, uint64_t
                         sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// The same for bf16 with a swizzle of its own.
+bool make_map_sw(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_in,
+                 uint32_t box_out, CUtensorMapSwizzle sw) {
+  std::memset(m, 0, sizeof(*m));
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {box_in, box_out};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The quantizer's view of a weight: a [nblocks, 64] bf16 matrix, loaded in boxes of
@@ -1118,7 +1134,20 @@ struct MultiPlan {
   size_t off_cnt = 0, off_list = 0, off_exp = 0, off_part = 0, off_ctr = 0;
   size_t off_pos = 0, off_perm = 0, off_slices = 0, off_nsl = 0, off_bt = 0;
   size_t off_pt = 0, off_gctr = 0, off_clear_end = 0, off_gpart = 0, total = 0;
+  // many tokens: the product over a 16-bit base (multi_mm.cuh); rp = operand columns per adapter
+  bool mm = false;
+  int rp = 64;
+  size_t off_w = 0, off_g = 0, off_bad = 0;
 };
+
+// Product for many tokens (multi_mm.cuh) or k_gemm's? The former costs writing the base in 16
+// bits and tiles of 256 tokens; its output rows must be 16-byte aligned, and its copies of the
+// adapters stay below the base's size.
+constexpr int64_t kMmMinTokens = 192;
+bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
+  return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K);
+}
+int stage_grid() { return num_sms() * 4; }
 
 constexpr uint32_t kProjRing = 104u * 1024u;  // with 2 CTAs per SM
 constexpr int kProjMaxCols = 128;             // slots x r16 of a batch: two accumulators of 128 columns
@@ -1147,9 +1176,18 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
   MultiPlan P;
   P.r16 = ((r + 15) / 16) * 16;
   P.per = 64 / P.r16;
-  P.tn = tn_for_tokens(M);
-  P.main = bwd ? plan_gemm(main_src, K, M, N, P.tn, 1, nsm) : plan_gemm(main_src, N, M, K, P.tn, 1, nsm);
-  P.tiles = P.main.col_tiles;
+  P.rp = r <= 16 ? 16 : (r <= 32 ? 32 : 64);
+  P.mm = use_mm(N, K, M, n, P.rp, bwd);
+  if (P.mm) {
+    P.tn = 256;
+    P.tiles = static_cast<int>((M + 255) / 256);
+    P.per = 1;
+  } else {
+    P.tn = tn_for_tokens(M);
+    P.main = bwd ? plan_gemm(main_src, K, M, N, P.tn, 1, nsm) : plan_gemm(main_src, N, M, K, P.tn, 1, nsm);
+    P.tiles = P.main.col_tiles;
+  }
+  const int width = P.mm ? P.rp : 64;
   P.dmax = static_cast<int>(std::min<int64_t>({n, P.tn, M}));
   P.cmax = (P.dmax + P.per - 1) / P.per;
   P.proj = plan_proj(M, (bwd ? std::min(N, K) : K) / 64, bwd ? 2 : 1, P.dmax, P.per, P.r16, nsm);
@@ -1161,9 +1199,15 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
   };
   P.off_cnt = take(static_cast<size_t>(P.tiles) * sizeof(int));
   P.off_list = take(static_cast<size_t>(P.tiles) * P.dmax * sizeof(int));
-  P.off_exp = take(static_cast<size_t>(P.tiles) * P.cmax * P.tn * 128);
+  P.off_exp = take(static_cast<size_t>(P.tiles) * P.cmax * P.tn * width * 2);
+  if (P.mm) {
+    const bool nf4 = main_src == A_NF4_K || main_src == A_NF4_MN;
+    P.off_w = take(nf4 ? static_cast<size_t>(N) * K * 2 : 0);
+    P.off_g = take(static_cast<size_t>(n) * P.rp * (bwd ? K : N) * 2);
+    P.off_bad = take(static_cast<size_t>(stage_grid()) * sizeof(int));
+  }
   P.off_part = take(P.main.part_floats() * sizeof(float));
-  P.off_ctr = take(static_cast<size_t>(P.main.tiles()) * sizeof(unsigned));
+  P.off_ctr = take(static_cast<size_t>(P.mm ? 0 : P.main.tiles()) * sizeof(unsigned));
   if (bwd) {
     P.ldp = (M + 63) / 64 * 64 + 64 * std::min<int64_t>(n, M);
     P.ftiles = static_cast<int>((K + 127) / 128 + (N + 127) / 128);
@@ -1240,7 +1284,7 @@ struct ProjJob {
 };
 
 qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const ProjJob* jobs, int njobs,
-                       uint8_t* w8, cudaStream_t s) {
+                       int lazy, uint8_t* w8, cudaStream_t s) {
   static thread_local ProjArgs g;
   std::memset(&g, 0, sizeof(g));
   for (int i = 0; i < njobs; ++i) {
@@ -1272,7 +1316,9 @@ qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const 
   g.cnt = reinterpret_cast<int*>(w8 + P.off_cnt);
   g.list = reinterpret_cast<int*>(w8 + P.off_list);
   g.ctr = reinterpret_cast<unsigned*>(w8 + P.off_ctr);
-  g.nctr = static_cast<int>(P.main.tiles());
+  g.nctr = P.mm ? 0 : static_cast<int>(P.main.tiles());
+  g.width = P.mm ? P.rp : 64;
+  g.lazy = lazy;
   g.wait_ns = g_wait_ns;
   launch_multi_kernel(k_multi_proj, g_proj_smem_set,
                       dim3(P.proj.slices, static_cast<unsigned>((M + 127) / 128), njobs * P.proj.nz), kMultiThreads,
@@ -1338,14 +1384,120 @@ qnf4_status multi_main(const BaseSrc& src, int main_src, const MultiPlan& P, con
   return st;
 }
 
+// Many tokens: the base in 16 bits and the adapters' second operand (rows cols as in StageArgs).
+qnf4_status multi_stage(const BaseSrc& src, const MultiPlan& P, const Adapters& ad, bool bwd, uint8_t* w8,
+                        cudaStream_t s) {
+  StageArgs g;
+  std::memset(&g, 0, sizeof(g));
+  if (src.w) {
+    g.packed = reinterpret_cast<const uint32_t*>(src.w->packed);
+    g.code2 = src.w->code2;
+    g.scale2 = src.w->scale2;
+    g.mean = src.w->mean;
+    g.n8 = src.N * src.K / 8;
+    g.W = reinterpret_cast<uint16_t*>(w8 + P.off_w);
+  }
+  g.src = static_cast<const uint16_t*>(bwd ? ad.A : ad.B);
+  g.dst = reinterpret_cast<uint16_t*>(w8 + P.off_g);
+  g.rows = bwd ? ad.n : static_cast<int64_t>(ad.n) * src.N;
+  g.cols = bwd ? src.K : 1;
+  g.r = ad.r;
+  g.rp = P.rp;
+  g.bad = reinterpret_cast<int*>(w8 + P.off_bad);
+  std::memcpy(g.levels, nf4_tables().levels, sizeof(g.levels));
+  launch_pdl(k_multi_stage, dim3(stage_grid()), dim3(256), 0, s, g);
+  return launched("multi_stage");
+}
+
+// CTA pairs of k_multi_mm that the device holds at once (one CTA per SM).
+template <bool MN>
+int mm_pairs() {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  int& c = cache[dev < 64 ? dev : 0];
+  if (c == 0) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(num_sms() / 2 * 2);
+    cfg.blockDim = dim3(kMultiThreads);
+    cfg.dynamicSmemBytes = kMmSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int k = 0;
+    if (cudaFuncSetAttribute(k_multi_mm<MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMmSmem)) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&k, k_multi_mm<MN>, &cfg) != cudaSuccess || k < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    c = k;
+  }
+  return c;
+}
+
+bool g_mm_smem_set[2][64] = {};
+
+template <bool MN>
+qnf4_status multi_mm(const BaseSrc& src, const MultiPlan& P, const Adapters& ad, const void* X, int64_t M, void* out,
+                     uint8_t* w8, cudaStream_t s) {
+  const int64_t N = src.N, K = src.K, F = MN ? K : N, C = MN ? N : K;
+  const void* W = src.w ? static_cast<const void*>(w8 + P.off_w) : src.Wd;
+  uint16_t* exp = reinterpret_cast<uint16_t*>(w8 + P.off_exp);
+  uint16_t* ag = reinterpret_cast<uint16_t*>(w8 + P.off_g);
+  static thread_local MmArgs g;
+  std::memset(&g, 0, sizeof(g));
+  const auto sw = P.rp == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : (P.rp == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!make_map(&g.tmX, X, false, C, M, C, 64, 128, true) || !make_map(&g.tmW, W, false, K, N, K, 64, MN ? 64 : 128, true) ||
+      !make_map_sw(&g.tmE, exp, P.rp, static_cast<uint64_t>(P.tiles) * P.dmax * 256, P.rp, P.rp, 128, sw) ||
+      !(MN ? make_map(&g.tmG, ag, false, K, static_cast<uint64_t>(ad.n) * P.rp, K, 64, P.rp, true)
+           : make_map_sw(&g.tmG, ag, P.rp, static_cast<uint64_t>(ad.n) * N, P.rp, P.rp, 128, sw)) ||
+      !make_map(&g.tmO, out, false, F, M, F, 64, 32, true))
+    return map_fail();
+  g.M = M;
+  g.F = F;
+  g.nk = static_cast<int>((C + 63) / 64);
+  g.tt = P.tiles;
+  g.ft = static_cast<int>((F + 255) / 256);
+  g.rp = P.rp;
+  g.dmax = P.dmax;
+  g.cnt = reinterpret_cast<const int*>(w8 + P.off_cnt);
+  g.list = reinterpret_cast<const int*>(w8 + P.off_list);
+  g.grows = MN ? P.rp : N;
+  g.bad = reinterpret_cast<const int*>(w8 + P.off_bad);
+  g.nbad = stage_grid();
+  g.ids = ad.ids;
+  g.ext = static_cast<const uint16_t*>(MN ? ad.A : ad.B);
+  g.exp = exp;
+  g.as = static_cast<int64_t>(ad.r) * (MN ? K : N);
+  g.js = MN ? K : ad.r;
+  g.r = ad.r;
+  g.n = ad.n;
+  g.wait_ns = g_wait_ns;
+  const int pairs = mm_pairs<MN>();
+  if (pairs < 1) return fail(QNF4_ERR_CUDA, "no CTA pair of the many-token product fits this device");
+  if (g_ev_start) cudaEventRecord(g_ev_start, s);
+  launch_multi_kernel(k_multi_mm<MN>, g_mm_smem_set[MN], dim3(2 * std::min(pairs, g.tt * g.ft)), kMultiThreads, kMmSmem, 2, s, g);
+  if (g_ev_stop) cudaEventRecord(g_ev_stop, s);
+  return launched("multi_mm");
+}
+
 qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int64_t M, void* h, void* ws,
                       size_t ws_bytes, cudaStream_t s) {
   const MultiPlan P = plan_multi(src.kind, src.N, src.K, M, ad.n, ad.r, false, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   const ProjJob job{x, ad.A, src.K, reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr};
-  const qnf4_status st = multi_proj(P, ad, M, &job, 1, w8, s);
+  qnf4_status st = P.mm ? multi_stage(src, P, ad, false, w8, s) : QNF4_OK;
+  if (st == QNF4_OK) st = multi_proj(P, ad, M, &job, 1, P.mm, w8, s);
   if (st != QNF4_OK) return st;
+  if (P.mm) return multi_mm<false>(src, P, ad, x, M, h, w8, s);
   return multi_main(src, src.kind, P, ad, x, M, ad.B, ad.r, src.N * ad.r, h, w8, s);
 }
 
@@ -1419,16 +1571,20 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   pr.N = N;
   pr.clear = reinterpret_cast<uint4*>(w8 + P.off_pt);
   pr.nclear = static_cast<int64_t>(P.off_clear_end - P.off_pt) / 16;
+  pr.lazy = P.mm;
+  qnf4_status st = P.mm ? multi_stage(src, P, ad, true, w8, s) : QNF4_OK;
+  if (st != QNF4_OK) return st;
   const int64_t blocks = std::max<int64_t>(ad.n * ((N + 63) / 64), 8);
   launch_pdl(k_multi_prep, dim3(1 + static_cast<unsigned>(std::min<int64_t>(blocks, num_sms()))), dim3(kPrepThreads),
              std::max<size_t>(static_cast<size_t>(ad.n) * (ad.n <= kPrepTable ? 136 : 8), 64u * (r + 1) * 2), s, pr);
-  qnf4_status st = launched("multi_prep");
+  st = launched("multi_prep");
   if (st != QNF4_OK) return st;
   const ProjJob jobs[2] = {{dY, bt, N, reinterpret_cast<uint16_t*>(w8 + P.off_exp), ptv}, {x, ad.A, K, nullptr, ptu}};
-  st = multi_proj(P, ad, M, jobs, 2, w8, s);
+  st = multi_proj(P, ad, M, jobs, 2, 0, w8, s);
   if (st != QNF4_OK) return st;
   st = multi_grad(P, ad, x, dY, M, N, K, ptv, ptu, dA, dB, w8, s);
   if (st != QNF4_OK) return st;
+  if (P.mm) return multi_mm<true>(src, P, ad, dY, M, dX, w8, s);
   return multi_main(src, main_src, P, ad, dY, M, ad.A, K, static_cast<int64_t>(r) * K, dX, w8, s);
 }
 

@@ -14,6 +14,8 @@
 //   k_multi_prep  (backward) tokens sorted by adapter, B transposed
 //   k_multi_proj  u = s x A^T and v = s dY B of every token's own adapter
 //   k_multi_grad  dA and dB, over the sorted tokens
+//
+// and, for many tokens, multi_mm.cuh has the product itself.
 #pragma once
 #include "common.cuh"
 #include "gemm.cuh"
@@ -68,13 +70,15 @@ constexpr int kFlushSteps = 4;
 struct ProjArgs {
   CUtensorMap tmX[2], tmF[2];  // X [M, C] in boxes of 128 x 64, F [n r, C] in boxes of r16 x 64
   int nsteps[2];
-  uint16_t* exp[2];            // operand blocks [tiles][cmax][tn][64], or null
+  uint16_t* exp[2];            // operand blocks [tiles][cmax][tn][width], or null
   uint16_t* pt[2];             // parts [3 r16][ldp], or null
   const int* ids;
   const float* scales;
   const int* pos;              // sorted position of each token
   int64_t M, ldp;
   int n, r, r16, per, tn, dmax, cmax;
+  int width;                   // columns of an operand block: 64, or the padded rank (per = 1)
+  int lazy;                    // the previous grid's results are not read here: wait for it at the end
   int sb, nz;                  // slots per batch; CTA z takes the batches z, z + nz, ...
   int slices;                  // cluster size
   uint32_t ring_bytes, tmem_cols;
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  griddep_wait();
+  if (!g.lazy) griddep_wait();
   griddep_launch_dependents();
 
   // the adapters of the column tile as a bit set; an adapter's slot is its rank in it
@@ -308,8 +312,9 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     const bool ok = !s_abort;
     if (ok && g.exp[job]) {
       const int c0 = first / g.per, nch = (nb + g.per - 1) / g.per;
-      for (int i = tid; i < share * nch * 8; i += kMultiThreads) {
-        const int q8 = i & 7, row = (i >> 3) / nch, c = (i >> 3) - row * nch;
+      const int w8 = g.width / 8;
+      for (int i = tid; i < share * nch * w8; i += kMultiThreads) {
+        const int q8 = i % w8, row = i / w8 / nch, c = i / w8 - row * nch;
         const int64_t m = row0 + r0 + row;
         const int p = 8 * q8 / r16, j = 8 * q8 - p * r16;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
                          pack_bf16x2(f[6], f[7]));
         }
         if (m < g.M)
-          *reinterpret_cast<uint4*>(g.exp[job] + (((tile * g.cmax + c0 + c) * g.tn + (m - tok0)) * 64 + 8 * q8)) = v;
+          *reinterpret_cast<uint4*>(g.exp[job] + (((tile * g.cmax + c0 + c) * g.tn + (m - tok0)) * g.width + 8 * q8)) = v;
       }
     }
     if (ok && g.pt[job]) {
@@ -345,6 +350,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     if (g.slices > 1) cluster_sync();
     __syncthreads();
   }
+  if (g.lazy) griddep_wait();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -385,6 +391,7 @@ struct PrepArgs {
   int64_t N;
   uint4* clear;      // 16-byte words to clear
   int64_t nclear;
+  int lazy;          // as in ProjArgs
 };
 
 constexpr int kPrepThreads = 1024;
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
   extern __shared__ int prep_sm[];
   __shared__ int s_warp[4][32];
   __shared__ int s_sum[4];
-  griddep_wait();
+  if (!g.lazy) griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x == 0) {
@@ -528,6 +535,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
       for (int p = end + lane; p < stop; p += 32)
         if (in_bounds(p < g.ldp, 94)) g.perm[p] = last;
     }
+    if (g.lazy) griddep_wait();
     return;
   }
   const int64_t nt = (g.N + 63) / 64;
@@ -547,6 +555,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
   for (int64_t i = static_cast<int64_t>(blockIdx.x - 1) * kPrepThreads + tid; i < g.nclear;
        i += static_cast<int64_t>(gridDim.x - 1) * kPrepThreads)
     g.clear[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (g.lazy) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
