@@ -299,9 +299,10 @@ struct GemmPlan {
   int ctas_per_sm = 1;
   int nset = 1;  // converter warp sets (4 warps each)
   int lut = 0;   // NF4 dequantization through the shared-memory pair table
+  int clus = 1;  // many adapters: the slices of a tile are the CTAs of a cluster (no partials)
   size_t smem = 0;
   size_t part_floats() const {
-    return tail_splits > 1 ? static_cast<size_t>(tail_tiles) * tail_splits * tn * 128 : 0;
+    return tail_splits > 1 && clus == 1 ? static_cast<size_t>(tail_tiles) * tail_splits * tn * 128 : 0;
   }
   int64_t tiles() const { return static_cast<int64_t>(row_tiles) * col_tiles; }
 };
@@ -486,6 +487,7 @@ qnf4_status launch_gemm(const GemmPlan& p, const CUtensorMap& a, const CUtensorM
   g.part_elems = static_cast<int64_t>(p.part_floats());
   g.cnt_elems = p.tail_tiles;
   g.wait_ns = g_wait_ns;
+  g.clus = p.clus;
   if (!p.has_ext) g.stage = 0;  // the staging buffers live in the adapter tile
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
@@ -494,11 +496,14 @@ qnf4_status launch_gemm(const GemmPlan& p, const CUtensorMap& a, const CUtensorM
   cfg.blockDim = dim3(gemm_threads(NSET), 1, 1);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.clus);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.clus > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_gemm<ASRC, NSET, MINB, MULTI>, a, b, bx, o, t, g);
   if (e != cudaSuccess) {
     g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -1149,12 +1154,7 @@ bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
 }
 int stage_grid() { return num_sms() * 4; }
 
-constexpr uint32_t kProjRing = 104u * 1024u;  // with 2 CTAs per SM
-constexpr int kProjMaxCols = 128;             // slots x r16 of a batch: two accumulators of 128 columns
-static_assert(3u * (16384u + kProjMaxCols * 128u) <= kProjRing, "three stages");
-static_assert(128u * 65u * 4u + 128u * 64u * 4u <= kProjRing, "the sums reuse the ring");
-
-// About two CTAs per SM: first by slices of the contraction (at least four steps each), then,
+// About two CTAs per SM: first by slices of the contraction (at least two steps each), then,
 // where few tokens name many adapters, by taking the batches of slots in parallel and making
 // them smaller. With 1024 tokens and more the token tiles fill the SMs, and a tile rarely
 // names more adapters than one batch holds, so its CTAs take the batches one after another.
@@ -1164,7 +1164,7 @@ ProjPlan plan_proj(int64_t M, int64_t csteps, int jobs, int dmax, int per, int r
   const int slots = (dmax + per - 1) / per * per;
   const int sbmax = kProjMaxCols / r16 / per * per;
   p.sb = std::min(slots, sbmax);
-  while (p.slices < 8 && tiles * p.slices < 2 * nsm && csteps / (2 * p.slices) >= 4) p.slices *= 2;
+  while (p.slices < 8 && tiles * p.slices < 2 * nsm && csteps / (2 * p.slices) >= 2) p.slices *= 2;
   auto batches = [&] { return (slots + p.sb - 1) / p.sb; };
   while (p.sb > per && tiles * p.slices * batches() < nsm) p.sb = std::max(per, p.sb / 2 / per * per);
   p.nz = static_cast<int>(std::min<int64_t>(batches(), std::max<int64_t>(1, 2 * nsm / (tiles * p.slices))));
@@ -1186,11 +1186,19 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
     P.tn = tn_for_tokens(M);
     P.main = bwd ? plan_gemm(main_src, K, M, N, P.tn, 1, nsm) : plan_gemm(main_src, N, M, K, P.tn, 1, nsm);
     P.tiles = P.main.col_tiles;
+    // Few tiles, all of them cut: the slices of each form a cluster (at most 8).
+    GemmPlan& m = P.main;
+    if (m.full_tiles == 0 && m.tail_splits > 1 && static_cast<size_t>(m.tn) * 512 + 1024 <= m.smem) {
+      m.tail_sps = (m.nsteps + std::min(8, m.tail_splits) - 1) / std::min(8, m.tail_splits);
+      m.tail_splits = (m.nsteps + m.tail_sps - 1) / m.tail_sps;
+      m.units = m.grid = m.tail_tiles * m.tail_splits;
+      m.clus = m.tail_splits;
+    }
   }
   const int width = P.mm ? P.rp : 64;
   P.dmax = static_cast<int>(std::min<int64_t>({n, P.tn, M}));
   P.cmax = (P.dmax + P.per - 1) / P.per;
-  P.proj = plan_proj(M, (bwd ? std::min(N, K) : K) / 64, bwd ? 2 : 1, P.dmax, P.per, P.r16, nsm);
+  P.proj = plan_proj(M, (bwd ? std::max(N, K) : K) / 64, bwd ? 2 : 1, P.dmax, P.per, P.r16, nsm);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1287,9 +1295,11 @@ qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const 
                        int lazy, uint8_t* w8, cudaStream_t s) {
   static thread_local ProjArgs g;
   std::memset(&g, 0, sizeof(g));
+  const int xrows = static_cast<int>(std::min<int64_t>(128, (M + 15) / 16 * 16));
+  g.xrows = xrows;
   for (int i = 0; i < njobs; ++i) {
     const ProjJob& j = jobs[i];
-    if (!make_map(&g.tmX[i], j.X, false, j.C, M, j.C, 64, 128, true) ||
+    if (!make_map(&g.tmX[i], j.X, false, j.C, M, j.C, 64, static_cast<uint32_t>(xrows), true) ||
         !make_map(&g.tmF[i], j.F, false, j.C, static_cast<uint64_t>(ad.n) * ad.r, j.C, 64, P.r16, true))
       return map_fail();
     g.nsteps[i] = static_cast<int>((j.C + 63) / 64);
@@ -1311,7 +1321,6 @@ qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const 
   g.sb = P.proj.sb;
   g.nz = P.proj.nz;
   g.slices = P.proj.slices;
-  g.ring_bytes = kProjRing;
   g.tmem_cols = P.proj.tmem;
   g.cnt = reinterpret_cast<int*>(w8 + P.off_cnt);
   g.list = reinterpret_cast<int*>(w8 + P.off_list);
@@ -1322,7 +1331,7 @@ qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const 
   g.wait_ns = g_wait_ns;
   launch_multi_kernel(k_multi_proj, g_proj_smem_set,
                       dim3(P.proj.slices, static_cast<unsigned>((M + 127) / 128), njobs * P.proj.nz), kMultiThreads,
-                      kProjRing + 1024, P.proj.slices, s, g);
+                      kProjSmem, P.proj.slices, s, g);
   return launched("multi_proj");
 }
 
@@ -1465,6 +1474,8 @@ qnf4_status multi_mm(const BaseSrc& src, const MultiPlan& P, const Adapters& ad,
   g.nk = static_cast<int>((C + 63) / 64);
   g.tt = P.tiles;
   g.ft = static_cast<int>((F + 255) / 256);
+  const int pairs = mm_pairs<MN>();
+  if (pairs < 1) return fail(QNF4_ERR_CUDA, "no CTA pair of the many-token product fits this device");
   g.rp = P.rp;
   g.dmax = P.dmax;
   g.cnt = reinterpret_cast<const int*>(w8 + P.off_cnt);
@@ -1480,8 +1491,6 @@ qnf4_status multi_mm(const BaseSrc& src, const MultiPlan& P, const Adapters& ad,
   g.r = ad.r;
   g.n = ad.n;
   g.wait_ns = g_wait_ns;
-  const int pairs = mm_pairs<MN>();
-  if (pairs < 1) return fail(QNF4_ERR_CUDA, "no CTA pair of the many-token product fits this device");
   if (g_ev_start) cudaEventRecord(g_ev_start, s);
   launch_multi_kernel(k_multi_mm<MN>, g_mm_smem_set[MN], dim3(2 * std::min(pairs, g.tt * g.ft)), kMultiThreads, kMmSmem, 2, s, g);
   if (g_ev_stop) cudaEventRecord(g_ev_stop, s);

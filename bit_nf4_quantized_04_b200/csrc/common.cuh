@@ -77,6 +77,11 @@ QNF4_DEV void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+// Expect more bytes in the current phase, without arriving.
+QNF4_DEV void mbar_expect_more(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
 // Test for the completion of the phase with the given parity (returns at once).
 QNF4_DEV bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -209,12 +214,25 @@ QNF4_DEV uint32_t cluster_rank() {
 QNF4_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// fp32 at this CTA's shared address `addr` in CTA `rank` of the cluster
-QNF4_DEV float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  float v;
+// The same in two halves: what a thread did before its arrival, every thread sees after its wait.
+QNF4_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+QNF4_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// a word at this CTA's shared address `addr` in CTA `rank` of the cluster
+QNF4_DEV uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
+  uint32_t a, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+// four fp32 at this CTA's (16-byte aligned) shared address `addr` in CTA `rank` of the cluster
+QNF4_DEV float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 

@@ -154,6 +154,7 @@ struct GemmArgs {
   const uint16_t* mt_exp; // Bext [column tiles][mt_cmax][tn][64]
   int64_t ext_as;
   int mt_n, mt_dmax, mt_cmax, mt_per, mt_r16;
+  int clus;               // > 1: no whole waves, and a tile's slices are the CTAs of a cluster
   int lazy_dep;           // programmatic dependent launch: 0 = every thread waits for the
                           // previous grid after the prologue; 1 = only the adapter chunk's
                           // copy waits (its operand is the one the previous grid writes)
@@ -392,8 +393,9 @@ QNF4_DEV Unit unit_of(const GemmArgs& g, int u) {
     sps = g.nsteps;
   } else {
     const int v = u - g.full_tiles;
-    w.pt = v % g.tail_tiles;
-    w.z = v / g.tail_tiles;
+    const bool clus = MULTI && g.clus > 1;
+    w.pt = clus ? v / g.tail_splits : v % g.tail_tiles;
+    w.z = clus ? v % g.tail_splits : v / g.tail_tiles;
     t = g.full_tiles + w.pt;
     w.splits = g.tail_splits;
     sps = g.tail_sps;
@@ -518,6 +520,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
   __shared__ volatile int s_abort;
   __shared__ int s_last;
   __shared__ float s_lv[16];
+  __shared__ int s_fixed;   // MULTI in clusters: the same of the CTA's one unit
   __shared__ int s_fix[2];  // MULTI, by unit parity: the unit zeroed a non-finite adapter entry
 
   const int warp = threadIdx.x >> 5;
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     mbar_init(&fin_bar, 1);
     s_abort = 0;
     s_last = 0;
-    s_fix[0] = s_fix[1] = 0;
+    s_fix[0] = s_fix[1] = s_fixed = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < 16) s_lv[threadIdx.x] = g.levels[threadIdx.x];
@@ -915,7 +918,20 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
       // the sets split the tile's columns in 16-column chunks
       const int nchunk = g.tn / 16;
-      if (w.splits == 1 && g.stage) {
+      if (MULTI && g.clus > 1) {
+        // this slice's sums as [column][row] into the idle rings; the cluster adds them up below
+        float* red = reinterpret_cast<float*>(base) + lrow;
+        for (int ck = set; ck < nchunk; ck += NSET) {
+          uint32_t r[16];
+          tmem_ld16(taddr + ck * 16, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) red[(ck * 16 + j) * 128] = __uint_as_float(r[j]);
+        }
+        if (ct == 0) s_fixed = fix;
+        tc_fence_before();
+        mbar_arrive(&acc_empty);
+      } else if (w.splits == 1 && g.stage) {
         // 8-column pieces (bf16, [8 columns][128 rows]) through two 2 KB buffers per
         // set in the adapter tile, which is idle from the unit's last MMA to the next
         // unit's adapter write; one thread of the set stores each piece by TMA.
@@ -1342,6 +1358,52 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, ncols);
+  }
+  if (MULTI && g.clus > 1) {
+    // Each CTA of the cluster adds up a share of the tile's columns over all slices, in slice
+    // order, four rows of a column per thread, straight from the others' shared memory. (Partial
+    // tiles through global memory with one CTA reading them all took about 12 us at 4 slices of
+    // 128 x 256; this takes 3.)
+    cluster_sync();
+    const Unit w = unit_of<MULTI>(g, u0);
+    const int share = (g.tn + g.clus - 1) / g.clus, c0 = w.z * share;
+    const int nc = min(share, g.tn - c0);
+    bool fix = false;
+    for (int p = 0; p < g.clus; ++p) fix |= ld_cluster_u32(smem_u32(&s_fixed), p) != 0u;
+    const uint32_t red = smem_u32(base);
+    uint16_t* o = static_cast<uint16_t*>(g.out);
+    for (int i = threadIdx.x; i < nc * 32; i += blockDim.x) {
+      const int64_t col = w.col0 + c0 + (i >> 5), row = w.row0 + 4 * (i & 31);
+      if (col >= g.cols || row >= g.rows) continue;
+      const uint32_t at = red + static_cast<uint32_t>((c0 + (i >> 5)) * 128 + 4 * (i & 31)) * 4u;
+      float4 p[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < g.clus) p[c] = ld_cluster_f4(at, static_cast<uint32_t>(c));
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < g.clus) {
+          v[0] += p[c].x;
+          v[1] += p[c].y;
+          v[2] += p[c].z;
+          v[3] += p[c].w;
+        }
+      if (fix) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += ext_fix<MN>(g, row + j, col, w.ct);
+      }
+      const int64_t to = col * g.o_cs + row;  // (rows are contiguous in out)
+      if ((g.rows & 3) == 0) {
+        if (in_bounds(to + 3 < g.out_elems, 28))
+          *reinterpret_cast<uint2*>(o + to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (row + j < g.rows && in_bounds(to + j < g.out_elems, 28)) o[to + j] = f2bf(v[j]);
+      }
+    }
+    cluster_sync();  // the others may still be reading this CTA's sums
   }
 }
 

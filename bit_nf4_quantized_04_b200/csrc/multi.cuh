@@ -62,13 +62,23 @@ QNF4_DEV void drain_ring(uint64_t* full, int issued, int nst, unsigned long long
 // So two accumulators take turns, kFlushSteps steps each, and the epilogue warps add them up in
 // registers with rounded fp32 additions while the other one fills.
 //
+// X does not depend on which adapters the tile names, so its first steps are on their way while
+// the CTA finds them out; X and the adapters' rows therefore have rings of their own, released
+// together.
+//
 // Outputs: the main product's operand blocks (bf16 s u, zeros in the other slots), the tile's
 // list of adapters, and for the gradients the values in three bf16 parts that add up to the
 // fp32 value (8 bits each), transposed to [3 r16][sorted token].
 constexpr int kFlushSteps = 4;
+constexpr uint32_t kProjXRing = 64u * 1024u;   // four steps of 128 rows, eight of at most 64
+constexpr uint32_t kProjFRing = 40u * 1024u;   // two steps of 128 adapter rows at least
+constexpr uint32_t kProjSmem = 1024u + kProjXRing + kProjFRing;  // two CTAs per SM
+constexpr int kProjMaxCols = 128;              // slots x r16 of a batch: two accumulators of 128 columns
+static_assert(2u * kProjMaxCols * 128u <= kProjFRing, "two steps of adapter rows");
+static_assert(128u * 68u * 4u + 128u * 64u * 4u <= kProjXRing + kProjFRing, "the sums reuse the rings");
 
 struct ProjArgs {
-  CUtensorMap tmX[2], tmF[2];  // X [M, C] in boxes of 128 x 64, F [n r, C] in boxes of r16 x 64
+  CUtensorMap tmX[2], tmF[2];  // X [M, C] in boxes of xrows x 64, F [n r, C] in boxes of r16 x 64
   int nsteps[2];
   uint16_t* exp[2];            // operand blocks [tiles][cmax][tn][width], or null
   uint16_t* pt[2];             // parts [3 r16][ldp], or null
@@ -81,7 +91,8 @@ struct ProjArgs {
   int lazy;                    // the previous grid's results are not read here: wait for it at the end
   int sb, nz;                  // slots per batch; CTA z takes the batches z, z + nz, ...
   int slices;                  // cluster size
-  uint32_t ring_bytes, tmem_cols;
+  int xrows;                   // rows of X fetched per step: 128, or fewer tokens rounded up to 16
+  uint32_t tmem_cols;
   int* cnt;                    // [tiles]
   int* list;                   // [tiles][dmax]
   unsigned* ctr;               // the main product's arrival counters, cleared here
@@ -134,6 +145,23 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   if (!g.lazy) griddep_wait();
   griddep_launch_dependents();
 
+  const int r16 = g.r16;
+  const uint32_t xbytes = static_cast<uint32_t>(g.xrows) * 128u;
+  const int nx = kProjXRing / xbytes < kMultiMaxStages ? static_cast<int>(kProjXRing / xbytes) : kMultiMaxStages;
+  const int per_slice = (g.nsteps[job] + g.slices - 1) / g.slices;
+  const int k0 = static_cast<int>(rank) * per_slice;
+  const int left = g.nsteps[job] - k0;
+  const int steps = left < 0 ? 0 : (left < per_slice ? left : per_slice);
+  // X of the first steps of the CTA's first batch (there may be none: then they are waited for
+  // at the end)
+  const int ahead = steps < nx ? steps : nx;
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < ahead; ++i) {
+      mbar_expect_more(&full[i], xbytes);
+      tma_load_2d(base + i * xbytes, &g.tmX[job], &full[i], (k0 + i) * 64, static_cast<int32_t>(row0));
+    }
+  }
+
   // the adapters of the column tile as a bit set; an adapter's slot is its rank in it
   const int64_t tok0 = tile * g.tn;
   const int ntok = static_cast<int>(g.M - tok0 < g.tn ? g.M - tok0 : g.tn);
@@ -171,17 +199,12 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     s_scale[tid] = live ? g.scales[a] : 0.f;
   }
 
-  // the ring's geometry is that of this CTA's first batch, its largest
-  const int r16 = g.r16;
+  // the adapters' ring is cut for this CTA's first batch, its largest
   const uint32_t fslot = static_cast<uint32_t>(r16) * 128u;
   const int nb0 = total - z * g.sb < g.sb ? total - z * g.sb : g.sb;
-  const uint32_t stage = 16384u + static_cast<uint32_t>(nb0 > 0 ? nb0 : 0) * fslot;
-  const int fit = static_cast<int>(g.ring_bytes / stage);
-  const int nst = fit < kMultiMaxStages ? fit : kMultiMaxStages;
-  const int per_slice = (g.nsteps[job] + g.slices - 1) / g.slices;
-  const int k0 = static_cast<int>(rank) * per_slice;
-  const int left = g.nsteps[job] - k0;
-  const int steps = left < 0 ? 0 : (left < per_slice ? left : per_slice);
+  const uint32_t fstage = static_cast<uint32_t>(nb0 > 0 ? nb0 : 1) * fslot;
+  const int nf = static_cast<int>(kProjFRing / fstage) < nx ? static_cast<int>(kProjFRing / fstage) : nx;
+  uint8_t* fring = base + kProjXRing;
   int it = 0, blk = 0;  // steps and accumulator turns of earlier batches
 
   for (int first = z * g.sb; first < total; first += g.nz * g.sb) {  // alike in the whole cluster
@@ -200,22 +223,31 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         int issued = it;
         bool all = true;
         for (int i = it; i < it + steps && all; ++i) {
-          const int s = i % nst;
+          const int s = i % nx;
+          // the step nf before has released its adapter rows (and so the one nx before its X);
           // every lane waits, so all of them leave together
-          const bool ok = i < nst || wait_or_abort(&empty[s], static_cast<uint32_t>(i / nst - 1) & 1u, g.wait_ns, &s_abort, 91, true);
+          const bool ok = i < nf || wait_or_abort(&empty[(i - nf) % nx], static_cast<uint32_t>((i - nf) / nx) & 1u, g.wait_ns, &s_abort, 91, true);
           all = __all_sync(0xffffffffu, ok);
           if (!all) break;
-          uint8_t* st = base + static_cast<uint32_t>(s) * stage;
           const int32_t c = (k0 + i - it) * 64;
+          const uint32_t fbytes = static_cast<uint32_t>(nb) * fslot;
           if (lane == 0) {
-            mbar_expect_tx(&full[s], 16384u + static_cast<uint32_t>(nb) * fslot);
-            tma_load_2d(st, &g.tmX[job], &full[s], c, static_cast<int32_t>(row0));
+            if (i < ahead) {  // X is on its way
+              mbar_expect_tx(&full[s], fbytes);
+            } else {
+              mbar_expect_tx(&full[s], xbytes + fbytes);
+              tma_load_2d(base + s * xbytes, &g.tmX[job], &full[s], c, static_cast<int32_t>(row0));
+            }
           }
           __syncwarp();
-          if (lane < nb) tma_load_2d(st + 16384 + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
+          if (lane < nb)
+            tma_load_2d(fring + static_cast<uint32_t>(i % nf) * fstage + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
           ++issued;
         }
-        if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 92);
+        if (!all && lane == 0) {
+          for (int i = issued; i < ahead; ++i) mbar_arrive(&full[i]);  // X alone completes these
+          drain_ring(full, issued < ahead ? ahead : issued, nx, g.wait_ns, 92);
+        }
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -224,15 +256,15 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         bool ok = true;
         int b = blk;
         for (int i = 0; i < steps && ok; ++i) {
-          const int s = (it + i) % nst, turn = i % kFlushSteps;
+          const int s = (it + i) % nx, turn = i % kFlushSteps;
           if (turn == 0 && b >= 2)
             ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 90);
-          ok = ok && wait_or_abort(&full[s], static_cast<uint32_t>((it + i) / nst) & 1u, g.wait_ns, &s_abort, 93);
+          ok = ok && wait_or_abort(&full[s], static_cast<uint32_t>((it + i) / nx) & 1u, g.wait_ns, &s_abort, 93);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(base) + static_cast<uint32_t>(s) * stage;
-          const uint64_t ad = smem_desc(st, 16, 1024, kLayoutSW128);
-          const uint64_t bd = smem_desc(st + 16384, 16, 1024, kLayoutSW128);
+          // (rows past xrows are whatever lies there: their products are not read)
+          const uint64_t ad = smem_desc(smem_u32(base) + static_cast<uint32_t>(s) * xbytes, 16, 1024, kLayoutSW128);
+          const uint64_t bd = smem_desc(smem_u32(fring) + static_cast<uint32_t>((it + i) % nf) * fstage, 16, 1024, kLayoutSW128);
           const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_ss(d, ad + 2u * kk, bd + 2u * kk, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
@@ -283,10 +315,10 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         mbar_arrive(&acc_free[b & 1]);
       }
       if (ok) {
-        float* part = reinterpret_cast<float*>(base) + row * (r16 + 1);
+        float* part = reinterpret_cast<float*>(base) + row * (r16 + 4);  // 16-byte rows, no bank conflicts
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c < r16) part[c] = sum[c];
+        for (int c = 0; c < 64; c += 4)
+          if (c < r16) *reinterpret_cast<float4*>(part + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
       }
     }
     it += steps;
@@ -295,20 +327,37 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     if (g.slices > 1) cluster_sync();
     // this CTA's share of the tokens, summed over the slices
     const int share = 128 / g.slices, r0 = static_cast<int>(rank) * share;
-    float* fin = reinterpret_cast<float*>(base + 128 * 65 * 4);
+    float* fin = reinterpret_cast<float*>(base + 128 * 68 * 4);
     const uint32_t part0 = smem_u32(base);
-    for (int i = tid; i < share * r16; i += kMultiThreads) {
-      const int row = r0 + i / r16, j = i % r16;
+    const int q4 = r16 / 4;
+    for (int i = tid; i < share * q4; i += kMultiThreads) {
+      const int row = r0 + i / q4, j = 4 * (i % q4);
       const int mine = s_slot[row] - first;
-      float v = 0.f;
-      if (mine >= 0 && mine < nb && j < g.r) {
-        const uint32_t at = part0 + static_cast<uint32_t>(row * (r16 + 1) + j) * 4u;
-        for (int c = 0; c < g.slices; ++c) v += ld_cluster_f32(at, static_cast<uint32_t>(c));
-        v *= s_scale[row];
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine >= 0 && mine < nb) {
+        const uint32_t at = part0 + static_cast<uint32_t>(row * (r16 + 4) + j) * 4u;
+        float4 p[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < g.slices) p[c] = ld_cluster_f4(at, static_cast<uint32_t>(c));
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < g.slices) {
+            v.x += p[c].x;
+            v.y += p[c].y;
+            v.z += p[c].z;
+            v.w += p[c].w;
+          }
+        const float sc = s_scale[row];
+        v.x = j < g.r ? v.x * sc : 0.f;
+        v.y = j + 1 < g.r ? v.y * sc : 0.f;
+        v.z = j + 2 < g.r ? v.z * sc : 0.f;
+        v.w = j + 3 < g.r ? v.w * sc : 0.f;
       }
-      fin[i] = v;
+      *reinterpret_cast<float4*>(fin + 4 * i) = v;
     }
     __syncthreads();
+    if (g.slices > 1) cluster_arrive();  // this CTA has read the others' sums
     const bool ok = !s_abort;
     if (ok && g.exp[job]) {
       const int c0 = first / g.per, nch = (nb + g.per - 1) / g.per;
@@ -345,10 +394,14 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         }
       }
     }
-    // the others may still be reading this CTA's sums, and the next batch's copies write there
+    // the others have read this CTA's sums: the next batch's copies write there
     fence_proxy_async();
-    if (g.slices > 1) cluster_sync();
+    if (g.slices > 1) cluster_wait();
     __syncthreads();
+  }
+  if (total <= z * g.sb && warp == 0 && lane == 0) {  // no batch: the first steps of X still land
+    for (int i = 0; i < ahead; ++i) mbar_arrive(&full[i]);
+    drain_ring(full, ahead, nx, g.wait_ns, 92);
   }
   if (g.lazy) griddep_wait();
   __syncthreads();

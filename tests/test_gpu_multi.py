@@ -335,3 +335,19 @@ def test_refusals_of_the_binding():
     with pytest.raises(ValueError):
         q.qlora_linear_multi_fwd_group([w], [torch.zeros(17, K, dtype=torch.bfloat16, device="cuda")],
                                        torch.zeros(17, dtype=torch.int32, device="cuda"), [A], [B], s)
+
+
+@pytest.mark.parametrize("case", [(1000, 704, 1100, 4, 16, "runs"), (2560, 1280, 2500, 3, 24, "runs"),
+                                  (256, 6400, 256, 2, 8, "runs"), (4864, 256, 1030, 5, 64, "runs"),
+                                  (4096, 1024, 4096, 3, 16, "runs")], ids=str)
+@pytest.mark.parametrize("kind", ["nf4", "dense"])
+def test_long_contractions_and_partial_tiles(case, kind):
+    # few tiles with long contractions, and sizes just past a tile; twice for equal bits
+    import bit_nf4_quantized_04_b200 as q
+    _check_fwd(q, kind, *case, 600)
+    _check_bwd(q, kind, *case, 610)
+    N, K, M, n, r, mix = case
+    x, A, B, dY, ids, s = _inputs(N, K, M, n, r, mix, 620)
+    base, _, fwd, bwd = _base(q, kind, synth.llama_weight((N, K), 620, device="cuda"))
+    one, two = [[fwd(base, x, ids, A, B, s), *bwd(base, x, dY, ids, A, B, s)] for _ in range(2)]
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
