@@ -1471,7 +1471,7 @@ qnf4_status multi_mm(const BaseSrc& src, const MultiPlan& P, const Adapters& ad,
     return map_fail();
   g.M = M;
   g.F = F;
-  g.nk = static_cast<int>((C + 63) / 64);
+  g.nk = static_cast<int>((C + 127) / 128);
   g.tt = P.tiles;
   g.ft = static_cast<int>((F + 255) / 256);
   const int pairs = mm_pairs<MN>();

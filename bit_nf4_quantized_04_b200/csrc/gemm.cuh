@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     // Decode tiles read 32 bytes of each of 128 rows per step, rows K/2 bytes apart:
     // first the whole warp asks L2 for every unit's row slices of this CTA (contiguous
     // per row), so DRAM streams whole row ranges instead of scattered 32-byte pieces.
-    if (ASRC == A_NF4_K && g.tn <= 32 && g.packed) {
+    if (!MULTI && ASRC == A_NF4_K && g.tn <= 32 && g.packed) {
       for (int u = u0; u < g.nunits; u += ustep) {
         const Unit w = unit_of<MULTI>(g, u);
         if (w.nst <= 0) continue;

@@ -45,6 +45,19 @@ QNF4_DEV void drain_ring(uint64_t* full, int issued, int nst, unsigned long long
   }
 }
 
+// A position in a ring of n slots: its slot and phase, advanced without a division (one on the
+// MMA thread's path costs more than the step's MMAs).
+struct RingPos {
+  int s = 0;
+  uint32_t ph = 0;
+  QNF4_DEV void next(int n) {
+    if (++s == n) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Projections onto the tokens' own adapters
 // ---------------------------------------------------------------------------
@@ -205,7 +218,9 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   const uint32_t fstage = static_cast<uint32_t>(nb0 > 0 ? nb0 : 1) * fslot;
   const int nf = static_cast<int>(kProjFRing / fstage) < nx ? static_cast<int>(kProjFRing / fstage) : nx;
   uint8_t* fring = base + kProjXRing;
-  int it = 0, blk = 0;  // steps and accumulator turns of earlier batches
+  int it = 0;  // steps of earlier batches
+  RingPos px, pf, pw;        // this warp's place in the rings: X, adapter rows, the step nf before
+  uint32_t turn_n = 0;       // accumulator turns so far
 
   for (int first = z * g.sb; first < total; first += g.nz * g.sb) {  // alike in the whole cluster
     const int nb = total - first < g.sb ? total - first : g.sb;
@@ -222,13 +237,15 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
       if (!s_abort) {
         int issued = it;
         bool all = true;
-        for (int i = it; i < it + steps && all; ++i) {
-          const int s = i % nx;
+        for (int i = it; i < it + steps && all; ++i, px.next(nx), pf.next(nf)) {
+          const int s = px.s;
           // the step nf before has released its adapter rows (and so the one nx before its X);
           // every lane waits, so all of them leave together
-          const bool ok = i < nf || wait_or_abort(&empty[(i - nf) % nx], static_cast<uint32_t>((i - nf) / nx) & 1u, g.wait_ns, &s_abort, 91, true);
-          all = __all_sync(0xffffffffu, ok);
-          if (!all) break;
+          if (i >= nf) {
+            all = __all_sync(0xffffffffu, wait_or_abort(&empty[pw.s], pw.ph, g.wait_ns, &s_abort, 91, true));
+            if (!all) break;
+            pw.next(nx);
+          }
           const int32_t c = (k0 + i - it) * 64;
           const uint32_t fbytes = static_cast<uint32_t>(nb) * fslot;
           if (lane == 0) {
@@ -241,7 +258,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
           }
           __syncwarp();
           if (lane < nb)
-            tma_load_2d(fring + static_cast<uint32_t>(i % nf) * fstage + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
+            tma_load_2d(fring + static_cast<uint32_t>(pf.s) * fstage + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
           ++issued;
         }
         if (!all && lane == 0) {
@@ -253,19 +270,21 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     } else if (warp == 1) {
       if (lane == 0 && !s_abort) {
         const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(nb * r16), 0u, 0u);
+        const uint64_t ad0 = smem_desc(smem_u32(base), 16, 1024, kLayoutSW128);
+        const uint64_t bd0 = smem_desc(smem_u32(fring), 16, 1024, kLayoutSW128);
         bool ok = true;
-        int b = blk;
-        for (int i = 0; i < steps && ok; ++i) {
-          const int s = (it + i) % nx, turn = i % kFlushSteps;
+        uint32_t b = turn_n;
+        for (int i = 0; i < steps && ok; ++i, px.next(nx), pf.next(nf)) {
+          const int s = px.s, turn = i % kFlushSteps;
           if (turn == 0 && b >= 2)
-            ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 90);
-          ok = ok && wait_or_abort(&full[s], static_cast<uint32_t>((it + i) / nx) & 1u, g.wait_ns, &s_abort, 93);
+            ok = wait_or_abort(&acc_free[b & 1], (b / 2 - 1) & 1u, g.wait_ns, &s_abort, 90);
+          ok = ok && wait_or_abort(&full[s], px.ph, g.wait_ns, &s_abort, 93);
           if (!ok) break;
           tc_fence_after();
           // (rows past xrows are whatever lies there: their products are not read)
-          const uint64_t ad = smem_desc(smem_u32(base) + static_cast<uint32_t>(s) * xbytes, 16, 1024, kLayoutSW128);
-          const uint64_t bd = smem_desc(smem_u32(fring) + static_cast<uint32_t>((it + i) % nf) * fstage, 16, 1024, kLayoutSW128);
-          const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
+          const uint64_t ad = ad0 + ((static_cast<uint32_t>(s) * xbytes) >> 4);
+          const uint64_t bd = bd0 + ((static_cast<uint32_t>(pf.s) * fstage) >> 4);
+          const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_ss(d, ad + 2u * kk, bd + 2u * kk, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&empty[s]);
@@ -291,11 +310,11 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
       const int turns = (steps + kFlushSteps - 1) / kFlushSteps;
       bool ok = !s_abort;
       for (int t = 0; t < turns && ok; ++t) {
-        const int b = blk + t;
-        ok = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], static_cast<uint32_t>(b / 2) & 1u, g.wait_ns, &s_abort, 94));
+        const uint32_t b = turn_n + t;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], (b / 2) & 1u, g.wait_ns, &s_abort, 94));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
         for (int sl = 0; sl < nb; ++sl) {
           if (!__any_sync(0xffffffffu, mine == sl)) continue;
 #pragma unroll
@@ -322,7 +341,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
       }
     }
     it += steps;
-    blk += (steps + kFlushSteps - 1) / kFlushSteps;
+    turn_n += (steps + kFlushSteps - 1) / kFlushSteps;
     __syncthreads();
     if (g.slices > 1) cluster_sync();
     // this CTA's share of the tokens, summed over the slices
@@ -687,10 +706,11 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
     if (warp == 0) {
       int issued = 0;
       bool all = true;
-      for (int i = 0; i < sl.steps && all; ++i) {
-        const int s = i % nst;
+      RingPos p;  // (the phase of a slot's previous use is the opposite one)
+      for (int i = 0; i < sl.steps && all; ++i, p.next(nst)) {
+        const int s = p.s;
         const int4 rows = *reinterpret_cast<const int4*>(g.perm + sl.p0 + i * 64 + (lane & 15) * 4);
-        const bool ok = i < nst || wait_or_abort(&empty[s], static_cast<uint32_t>(i / nst - 1) & 1u, g.wait_ns, &s_abort, 96, true);
+        const bool ok = i < nst || wait_or_abort(&empty[s], p.ph ^ 1u, g.wait_ns, &s_abort, 96, true);
         all = __all_sync(0xffffffffu, ok);
         if (!all) break;
         uint8_t* st = base + static_cast<uint32_t>(s) * stage;
@@ -713,18 +733,20 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
       if (lane == 0) {
         const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
         const uint32_t pstep = (static_cast<uint32_t>(r16) * 128u) >> 4;  // descriptor units per part
+        const uint64_t ad0 = smem_desc(smem_u32(base), 8192, 1024, kLayoutSW128);
+        const uint64_t bd0 = smem_desc(smem_u32(base) + 16384, 16, 1024, kLayoutSW128);
         bool ok = true;
         int b = 0;
-        for (int i = 0; i < sl.steps && ok; ++i) {
-          const int s = i % nst, turn = i % kFlushSteps;
+        RingPos p;
+        for (int i = 0; i < sl.steps && ok; ++i, p.next(nst)) {
+          const int s = p.s, turn = i % kFlushSteps;
           if (turn == 0 && b >= 2)
             ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 89);
-          ok = ok && wait_or_abort(&full[s], static_cast<uint32_t>(i / nst) & 1u, g.wait_ns, &s_abort, 98);
+          ok = ok && wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 98);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(base) + static_cast<uint32_t>(s) * stage;
-          const uint64_t ad = smem_desc(st, 8192, 1024, kLayoutSW128);
-          const uint64_t bd = smem_desc(st + 16384, 16, 1024, kLayoutSW128);
+          const uint32_t so = (static_cast<uint32_t>(s) * stage) >> 4;
+          const uint64_t ad = ad0 + so, bd = bd0 + so;
           const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {

@@ -161,8 +161,13 @@ __global__ void __launch_bounds__(256) k_multi_stage(const __grid_constant__ Sta
 // ---------------------------------------------------------------------------
 // The product
 // ---------------------------------------------------------------------------
-constexpr int kMmStages = 6;
-constexpr uint32_t kMmStage = 32768u;                 // per CTA: 128 x 64 of X, 128 x 64 of W
+// A stage is 128 of the contraction: the one thread that issues the MMAs spends about 590 cycles
+// on a stage of 64 (barrier test 120, four MMAs 270, commit 80, loop 100) that holds 512 cycles of
+// tensor work, so that it, not the tensor cores, set the pace; eight MMAs per barrier reverse
+// that. An odd last half is zero fill.
+constexpr int kMmStages = 3;
+constexpr uint32_t kMmHalf = 32768u;                  // per CTA: 128 x 64 of X, 128 x 64 of W
+constexpr uint32_t kMmStage = 2u * kMmHalf;
 constexpr uint32_t kMmOut = 4u * 2u * 4096u;          // per epilogue warp two 32 x 64 pieces
 constexpr size_t kMmSmem = 1024 + kMmStages * kMmStage + kMmOut;
 constexpr int kMmGroup = 8;  // token tiles that share a sweep over the features (L2 reuse)
@@ -174,7 +179,7 @@ struct MmArgs {
   CUtensorMap tmG;  // adapter rows [n N, rp]: 128 x rp; or [n rp, K]: rp x 64
   CUtensorMap tmO;  // out [M, F]: boxes of 32 x 64
   int64_t M, F;
-  int nk;           // 64-wide steps of the contraction
+  int nk;           // 128-wide steps of the contraction
   int tt, ft;       // tiles of 256 tokens, of 256 features
   int rp, dmax;
   const int* cnt;   // [tt] adapters of a tile
@@ -289,12 +294,17 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
           const uint32_t bar = map_to_cta(&full[s], 0);
           if (i < g.nk) {
             if (rank == 0) mbar_expect_tx(&full[s], 2u * kMmStage);
-            tma_load_2d_pair(st, &g.tmX, bar, i * 64, tok);
-            if (!MN) {
-              tma_load_2d_pair(st + 16384, &g.tmW, bar, i * 64, feat);
-            } else {
-              tma_load_2d_pair(st + 16384, &g.tmW, bar, feat, i * 64);
-              tma_load_2d_pair(st + 24576, &g.tmW, bar, feat + 64, i * 64);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint8_t* sh = st + h * kMmHalf;
+              const int32_t c = i * 128 + h * 64;
+              tma_load_2d_pair(sh, &g.tmX, bar, c, tok);
+              if (!MN) {
+                tma_load_2d_pair(sh + 16384, &g.tmW, bar, c, feat);
+              } else {
+                tma_load_2d_pair(sh + 16384, &g.tmW, bar, feat, c);
+                tma_load_2d_pair(sh + 24576, &g.tmW, bar, feat + 64, c);
+              }
             }
           } else {
             const int x = i - g.nk, a = g.list[static_cast<int64_t>(t) * g.dmax + x];
@@ -319,7 +329,13 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
       const uint32_t idesc = idesc_bf16(256, 256, 0u, MN ? 1u : 0u);
       const uint32_t lay = g.rp == 16 ? 6u : (g.rp == 32 ? 4u : 2u);  // 32-, 64-, 128-byte swizzle
       const uint32_t rowb = 2u * static_cast<uint32_t>(g.rp);
-      int it = 0, k = 0;
+      const uint32_t smb = smem_u32(base);
+      const uint64_t ad0 = smem_desc(smb, 16, 1024, kLayoutSW128);
+      const uint64_t bd0 = MN ? smem_desc(smb + 16384, 8192, 1024, kLayoutSW128) : smem_desc(smb + 16384, 16, 1024, kLayoutSW128);
+      const uint64_t ae0 = smem_desc(smb, 16, 8u * rowb, lay);
+      const uint64_t be0 = MN ? smem_desc(smb + 16384, 64u * rowb, 1024, kLayoutSW128) : smem_desc(smb + 16384, 16, 8u * rowb, lay);
+      RingPos p;
+      int k = 0;
       bool ok = true;
       for (int u = pair; u < tiles && ok; u += npair, ++k) {
         int t, f;
@@ -329,21 +345,21 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(k & 1) * 256u;
-        for (int i = 0; i < g.nk + nx; ++i, ++it) {
-          const int s = it % kMmStages;
-          ok = wait_or_abort(&full[s], static_cast<uint32_t>(it / kMmStages) & 1u, g.wait_ns, &s_abort, 104);
+        for (int i = 0; i < g.nk + nx; ++i, p.next(kMmStages)) {
+          const int s = p.s;
+          ok = wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 104);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(base) + static_cast<uint32_t>(s) * kMmStage;
+          const uint32_t so = static_cast<uint32_t>(s) * (kMmStage >> 4);
           if (i < g.nk) {
-            const uint64_t ad = smem_desc(st, 16, 1024, kLayoutSW128);
-            const uint64_t bd = MN ? smem_desc(st + 16384, 8192, 1024, kLayoutSW128) : smem_desc(st + 16384, 16, 1024, kLayoutSW128);
+            const uint64_t ad = ad0 + so, bd = bd0 + so;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma2_ss(d, ad + 2u * kk, bd + (MN ? (2048u >> 4) : 2u) * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t h = (kk >> 2) * (kMmHalf >> 4), k4 = kk & 3;
+              mma2_ss(d, ad + h + 2u * k4, bd + h + (MN ? (2048u >> 4) : 2u) * k4, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            }
           } else {
-            const uint64_t ad = smem_desc(st, 16, 8u * rowb, lay);
-            const uint64_t bd = MN ? smem_desc(st + 16384, 64u * rowb, 1024, kLayoutSW128) : smem_desc(st + 16384, 16, 8u * rowb, lay);
+            const uint64_t ad = ae0 + so, bd = be0 + so;
             for (int kk = 0; kk < g.rp / 16; ++kk) mma2_ss(d, ad + 2u * kk, bd + (MN ? (2048u >> 4) : 2u) * kk, idesc, 1u);
           }
           mma2_commit(&empty[s]);
