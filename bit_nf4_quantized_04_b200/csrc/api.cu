@@ -1154,7 +1154,8 @@ bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
 }
 int stage_grid() { return num_sms() * 4; }
 
-// About two CTAs per SM: first by slices of the contraction (at least two steps each), then,
+// At most two CTAs per SM, all at once (a CTA costs about 6 us beside its steps, so a second wave
+// of shorter ones loses): first by slices of the contraction (at least two steps each), then,
 // where few tokens name many adapters, by taking the batches of slots in parallel and making
 // them smaller. With 1024 tokens and more the token tiles fill the SMs, and a tile rarely
 // names more adapters than one batch holds, so its CTAs take the batches one after another.
@@ -1164,7 +1165,7 @@ ProjPlan plan_proj(int64_t M, int64_t csteps, int jobs, int dmax, int per, int r
   const int slots = (dmax + per - 1) / per * per;
   const int sbmax = kProjMaxCols / r16 / per * per;
   p.sb = std::min(slots, sbmax);
-  while (p.slices < 8 && tiles * p.slices < 2 * nsm && csteps / (2 * p.slices) >= 2) p.slices *= 2;
+  while (p.slices < 8 && tiles * 2 * p.slices <= 2 * nsm && csteps / (2 * p.slices) >= 2) p.slices *= 2;
   auto batches = [&] { return (slots + p.sb - 1) / p.sb; };
   while (p.sb > per && tiles * p.slices * batches() < nsm) p.sb = std::max(per, p.sb / 2 / per * per);
   p.nz = static_cast<int>(std::min<int64_t>(batches(), std::max<int64_t>(1, 2 * nsm / (tiles * p.slices))));
@@ -1219,8 +1220,9 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
   if (bwd) {
     P.ldp = (M + 63) / 64 * 64 + 64 * std::min<int64_t>(n, M);
     P.ftiles = static_cast<int>((K + 127) / 128 + (N + 127) / 128);
-    // slices of 4 to 32 steps: about two CTAs per SM
-    P.lsteps = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(32, M * P.ftiles / (64 * 2 * nsm))));
+    // slices of 8 to 64 steps, twice as long as would make one wave of two CTAs per SM out of one
+    // adapter: several adapters are that many slices to begin with
+    P.lsteps = static_cast<int>(std::max<int64_t>(8, std::min<int64_t>(64, 2 * M * P.ftiles / (64 * 2 * nsm))));
     const int64_t several = M / (64 * P.lsteps);  // adapters of more than one slice, at most
     P.slmax = static_cast<int>(several + n);
     P.part_elems = 2 * several * P.ftiles * 128 * P.r16;
@@ -1519,6 +1521,7 @@ qnf4_status multi_grad(const MultiPlan& P, const Adapters& ad, const void* x, co
   std::memset(&g, 0, sizeof(g));
   const int64_t r = ad.r;
   if (!make_map(&g.tmX[0], x, false, K, M, K, 64, 1, true) || !make_map(&g.tmX[1], dY, false, N, M, N, 64, 1, true) ||
+      !make_map(&g.tmR[0], x, false, K, M, K, 64, 64, true) || !make_map(&g.tmR[1], dY, false, N, M, N, 64, 64, true) ||
       !make_map(&g.tmP[0], ptv, false, P.ldp, 3 * P.r16, P.ldp, 64, 3 * P.r16, true) ||
       !make_map(&g.tmP[1], ptu, false, P.ldp, 3 * P.r16, P.ldp, 64, 3 * P.r16, true))
     return map_fail();

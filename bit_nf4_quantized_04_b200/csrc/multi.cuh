@@ -62,8 +62,7 @@ struct RingPos {
 // Projections onto the tokens' own adapters
 // ---------------------------------------------------------------------------
 // P[m][0 .. r) = scales[a] sum_c X[m, c] F[a][0 .. r)[c]. A CTA takes 128 tokens, a batch of the
-// adapters that their column tile of the main product names (its slots) and a slice of the
-// contraction; X and the adapters' rows come by TMA (128-byte swizzle), one MMA of N = slots x
+// adapters that they name (its slots) and a slice of the contraction; X and the adapters' rows come by TMA (128-byte swizzle), one MMA of N = slots x
 // r16 multiplies every token with every slot, and the epilogue keeps each token's own slot:
 // with a few slots per tile the extra products cost nothing beside the stream of X, and rows
 // of different tokens or adapters never mix. The slices of a contraction are the CTAs of a
@@ -76,19 +75,18 @@ struct RingPos {
 // registers with rounded fp32 additions while the other one fills.
 //
 // X does not depend on which adapters the tile names, so its first steps are on their way while
-// the CTA finds them out; X and the adapters' rows therefore have rings of their own, released
-// together.
+// the CTA finds them out; X and the adapters' rows therefore have rings of their own, from either
+// end of one buffer, of as many steps as fit once the number of slots is known.
 //
 // Outputs: the main product's operand blocks (bf16 s u, zeros in the other slots), the tile's
 // list of adapters, and for the gradients the values in three bf16 parts that add up to the
 // fp32 value (8 bits each), transposed to [3 r16][sorted token].
 constexpr int kFlushSteps = 4;
-constexpr uint32_t kProjXRing = 64u * 1024u;   // four steps of 128 rows, eight of at most 64
-constexpr uint32_t kProjFRing = 40u * 1024u;   // two steps of 128 adapter rows at least
-constexpr uint32_t kProjSmem = 1024u + kProjXRing + kProjFRing;  // two CTAs per SM
+constexpr uint32_t kProjRing = 104u * 1024u;
+constexpr uint32_t kProjSmem = 1024u + kProjRing;  // two CTAs per SM
 constexpr int kProjMaxCols = 128;              // slots x r16 of a batch: two accumulators of 128 columns
-static_assert(2u * kProjMaxCols * 128u <= kProjFRing, "two steps of adapter rows");
-static_assert(128u * 68u * 4u + 128u * 64u * 4u <= kProjXRing + kProjFRing, "the sums reuse the rings");
+static_assert(3u * (16384u + kProjMaxCols * 128u) <= kProjRing, "three steps");
+static_assert(128u * 68u * 4u + 128u * 64u * 4u <= kProjRing, "the sums reuse the rings");
 
 struct ProjArgs {
   CUtensorMap tmX[2], tmF[2];  // X [M, C] in boxes of xrows x 64, F [n r, C] in boxes of r16 x 64
@@ -118,10 +116,10 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   __shared__ __align__(8) uint64_t full[kMultiMaxStages], empty[kMultiMaxStages], acc_full[2], acc_free[2], fin_bar;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ uint32_t s_mask[kMultiMaxAdapters / 32];
-  __shared__ int s_pre[kMultiMaxAdapters / 32];
-  __shared__ int s_total;
-  __shared__ int s_slot[128], s_ad[16];
+  __shared__ uint32_t s_mask[kMultiMaxAdapters / 32], s_own[kMultiMaxAdapters / 32];
+  __shared__ int s_pre[kMultiMaxAdapters / 32], s_opre[kMultiMaxAdapters / 32];
+  __shared__ int s_total, s_ototal;
+  __shared__ int s_slot[128], s_tslot[128], s_ad[16];
   __shared__ float s_scale[128];
   uint8_t* base = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -151,7 +149,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     tmem_relinquish();
     tc_fence_before();
   }
-  for (int i = tid; i < words; i += kMultiThreads) s_mask[i] = 0u;
+  for (int i = tid; i < words; i += kMultiThreads) s_mask[i] = s_own[i] = 0u;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -160,14 +158,16 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 
   const int r16 = g.r16;
   const uint32_t xbytes = static_cast<uint32_t>(g.xrows) * 128u;
-  const int nx = kProjXRing / xbytes < kMultiMaxStages ? static_cast<int>(kProjXRing / xbytes) : kMultiMaxStages;
   const int per_slice = (g.nsteps[job] + g.slices - 1) / g.slices;
   const int k0 = static_cast<int>(rank) * per_slice;
   const int left = g.nsteps[job] - k0;
   const int steps = left < 0 ? 0 : (left < per_slice ? left : per_slice);
   // X of the first steps of the CTA's first batch (there may be none: then they are waited for
   // at the end)
-  const int ahead = steps < nx ? steps : nx;
+  const uint32_t fmost = static_cast<uint32_t>(g.sb * r16) * 128u;
+  const int least = static_cast<int>(kProjRing / (xbytes + fmost)) < kMultiMaxStages
+                        ? static_cast<int>(kProjRing / (xbytes + fmost)) : kMultiMaxStages;
+  const int ahead = steps < least ? steps : least;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < ahead; ++i) {
       mbar_expect_more(&full[i], xbytes);
@@ -175,76 +175,86 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     }
   }
 
-  // the adapters of the column tile as a bit set; an adapter's slot is its rank in it
+  // the adapters of the column tile as a bit set, in which an adapter's rank is its place in the
+  // main product's operand, and those of the CTA's own tokens, whose ranks are the slots here
   const int64_t tok0 = tile * g.tn;
   const int ntok = static_cast<int>(g.M - tok0 < g.tn ? g.M - tok0 : g.tn);
   for (int i = tid; i < ntok; i += kMultiThreads) {
     const uint32_t a = static_cast<uint32_t>(g.ids[tok0 + i]);
-    if (a < static_cast<uint32_t>(g.n)) atomicOr(&s_mask[a >> 5], 1u << (a & 31));
+    if (a < static_cast<uint32_t>(g.n)) {
+      atomicOr(&s_mask[a >> 5], 1u << (a & 31));
+      if (static_cast<uint64_t>(tok0 + i - row0) < 128u) atomicOr(&s_own[a >> 5], 1u << (a & 31));
+    }
   }
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
     for (int i = tid; i < g.nctr; i += kMultiThreads) g.ctr[i] = 0u;
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
+    const uint32_t* mask = warp == 0 ? s_mask : s_own;
+    int* pre = warp == 0 ? s_pre : s_opre;
     int before = 0;
     for (int w0 = 0; w0 < words; w0 += 32) {
-      const int c = w0 + lane < words ? __popc(s_mask[w0 + lane]) : 0;
+      const int c = w0 + lane < words ? __popc(mask[w0 + lane]) : 0;
       int inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      if (w0 + lane < words) s_pre[w0 + lane] = before + inc - c;
+      if (w0 + lane < words) pre[w0 + lane] = before + inc - c;
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) s_total = before;
+    if (lane == 0) (warp == 0 ? s_total : s_ototal) = before;
   }
   __syncthreads();
-  const int total = s_total;
+  const int ttotal = s_total, total = s_ototal;  // of the tile, of the CTA's tokens
   const bool lists = z == 0 && job == 0 && blockIdx.x == 0 && row0 == tok0;
-  if (lists && tid == 0) g.cnt[tile] = total;
+  if (lists) {
+    if (tid == 0) g.cnt[tile] = ttotal;
+    for (int w = tid; w < words; w += kMultiThreads) {
+      int s = s_pre[w];
+      for (uint32_t m = s_mask[w]; m; m &= m - 1, ++s)
+        if (in_bounds(s < g.dmax, 91)) g.list[tile * g.dmax + s] = w * 32 + __ffs(m) - 1;
+    }
+  }
   if (tid < 128) {
     const int64_t m = row0 + tid;
     const uint32_t a = m < g.M ? static_cast<uint32_t>(g.ids[m]) : 0xffffffffu;
     const bool live = a < static_cast<uint32_t>(g.n);
-    s_slot[tid] = live ? s_pre[a >> 5] + __popc(s_mask[a >> 5] & ((1u << (a & 31)) - 1u)) : -1;
+    const uint32_t below = (1u << (a & 31)) - 1u;
+    s_slot[tid] = live ? s_opre[a >> 5] + __popc(s_own[a >> 5] & below) : -1;
+    s_tslot[tid] = live ? s_pre[a >> 5] + __popc(s_mask[a >> 5] & below) : -1;
     s_scale[tid] = live ? g.scales[a] : 0.f;
   }
 
-  // the adapters' ring is cut for this CTA's first batch, its largest
+  // the rings are cut for this CTA's first batch, its largest
   const uint32_t fslot = static_cast<uint32_t>(r16) * 128u;
   const int nb0 = total - z * g.sb < g.sb ? total - z * g.sb : g.sb;
   const uint32_t fstage = static_cast<uint32_t>(nb0 > 0 ? nb0 : 1) * fslot;
-  const int nf = static_cast<int>(kProjFRing / fstage) < nx ? static_cast<int>(kProjFRing / fstage) : nx;
-  uint8_t* fring = base + kProjXRing;
+  const int fit = static_cast<int>(kProjRing / (xbytes + fstage));
+  const int nst = fit < kMultiMaxStages ? fit : kMultiMaxStages;
+  uint8_t* fring = base + kProjRing - static_cast<uint32_t>(nst) * fstage;
   int it = 0;  // steps of earlier batches
-  RingPos px, pf, pw;        // this warp's place in the rings: X, adapter rows, the step nf before
+  RingPos pos;               // this warp's place in the rings
   uint32_t turn_n = 0;       // accumulator turns so far
 
   for (int first = z * g.sb; first < total; first += g.nz * g.sb) {  // alike in the whole cluster
     const int nb = total - first < g.sb ? total - first : g.sb;
     for (int w = tid; w < words; w += kMultiThreads) {
-      int s = s_pre[w];
-      for (uint32_t m = s_mask[w]; m; m &= m - 1, ++s) {
-        const int a = w * 32 + __ffs(m) - 1;
-        if (s >= first && s < first + nb) s_ad[s - first] = a;
-        if (lists && first == 0 && in_bounds(s < g.dmax, 91)) g.list[tile * g.dmax + s] = a;
-      }
+      int s = s_opre[w];
+      for (uint32_t m = s_own[w]; m; m &= m - 1, ++s)
+        if (s >= first && s < first + nb) s_ad[s - first] = w * 32 + __ffs(m) - 1;
     }
     __syncthreads();
     if (warp == 0) {
       if (!s_abort) {
         int issued = it;
         bool all = true;
-        for (int i = it; i < it + steps && all; ++i, px.next(nx), pf.next(nf)) {
-          const int s = px.s;
-          // the step nf before has released its adapter rows (and so the one nx before its X);
-          // every lane waits, so all of them leave together
-          if (i >= nf) {
-            all = __all_sync(0xffffffffu, wait_or_abort(&empty[pw.s], pw.ph, g.wait_ns, &s_abort, 91, true));
+        for (int i = it; i < it + steps && all; ++i, pos.next(nst)) {
+          const int s = pos.s;
+          if (i >= nst) {  // every lane waits, so all of them leave together
+            all = __all_sync(0xffffffffu, wait_or_abort(&empty[s], pos.ph ^ 1u, g.wait_ns, &s_abort, 91, true));
             if (!all) break;
-            pw.next(nx);
           }
           const int32_t c = (k0 + i - it) * 64;
           const uint32_t fbytes = static_cast<uint32_t>(nb) * fslot;
@@ -258,12 +268,12 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
           }
           __syncwarp();
           if (lane < nb)
-            tma_load_2d(fring + static_cast<uint32_t>(pf.s) * fstage + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
+            tma_load_2d(fring + static_cast<uint32_t>(s) * fstage + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
           ++issued;
         }
         if (!all && lane == 0) {
           for (int i = issued; i < ahead; ++i) mbar_arrive(&full[i]);  // X alone completes these
-          drain_ring(full, issued < ahead ? ahead : issued, nx, g.wait_ns, 92);
+          drain_ring(full, issued < ahead ? ahead : issued, nst, g.wait_ns, 92);
         }
       }
       __syncwarp();
@@ -274,16 +284,16 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         const uint64_t bd0 = smem_desc(smem_u32(fring), 16, 1024, kLayoutSW128);
         bool ok = true;
         uint32_t b = turn_n;
-        for (int i = 0; i < steps && ok; ++i, px.next(nx), pf.next(nf)) {
-          const int s = px.s, turn = i % kFlushSteps;
+        for (int i = 0; i < steps && ok; ++i, pos.next(nst)) {
+          const int s = pos.s, turn = i % kFlushSteps;
           if (turn == 0 && b >= 2)
             ok = wait_or_abort(&acc_free[b & 1], (b / 2 - 1) & 1u, g.wait_ns, &s_abort, 90);
-          ok = ok && wait_or_abort(&full[s], px.ph, g.wait_ns, &s_abort, 93);
+          ok = ok && wait_or_abort(&full[s], pos.ph, g.wait_ns, &s_abort, 93);
           if (!ok) break;
           tc_fence_after();
           // (rows past xrows are whatever lies there: their products are not read)
           const uint64_t ad = ad0 + ((static_cast<uint32_t>(s) * xbytes) >> 4);
-          const uint64_t bd = bd0 + ((static_cast<uint32_t>(pf.s) * fstage) >> 4);
+          const uint64_t bd = bd0 + ((static_cast<uint32_t>(s) * fstage) >> 4);
           const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_ss(d, ad + 2u * kk, bd + 2u * kk, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
@@ -379,20 +389,23 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     if (g.slices > 1) cluster_arrive();  // this CTA has read the others' sums
     const bool ok = !s_abort;
     if (ok && g.exp[job]) {
-      const int c0 = first / g.per, nch = (nb + g.per - 1) / g.per;
+      // the tokens of this batch, and with the first batch those without an adapter: their rows
+      // of every block of the tile, zeros but in their own adapter's place
+      const int nch = (ttotal + g.per - 1) / g.per;
       const int w8 = g.width / 8;
       for (int i = tid; i < share * nch * w8; i += kMultiThreads) {
         const int q8 = i % w8, row = i / w8 / nch, c = i / w8 - row * nch;
         const int64_t m = row0 + r0 + row;
+        const int mine = s_slot[r0 + row] - first, ts = s_tslot[r0 + row];
+        if (m >= g.M || !(ts < 0 ? first == 0 : mine >= 0 && mine < nb)) continue;
         const int p = 8 * q8 / r16, j = 8 * q8 - p * r16;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (p < g.per && s_slot[r0 + row] - first == c * g.per + p) {
+        if (p < g.per && ts == c * g.per + p) {
           const float* f = fin + row * r16 + j;
           v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                          pack_bf16x2(f[6], f[7]));
         }
-        if (m < g.M)
-          *reinterpret_cast<uint4*>(g.exp[job] + (((tile * g.cmax + c0 + c) * g.tn + (m - tok0)) * g.width + 8 * q8)) = v;
+        *reinterpret_cast<uint4*>(g.exp[job] + (((tile * g.cmax + c) * g.tn + (m - tok0)) * g.width + 8 * q8)) = v;
       }
     }
     if (ok && g.pt[job]) {
@@ -420,7 +433,17 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   }
   if (total <= z * g.sb && warp == 0 && lane == 0) {  // no batch: the first steps of X still land
     for (int i = 0; i < ahead; ++i) mbar_arrive(&full[i]);
-    drain_ring(full, ahead, nx, g.wait_ns, 92);
+    drain_ring(full, ahead, nst, g.wait_ns, 92);
+  }
+  if (total == 0 && ttotal > 0 && z == 0 && rank == 0 && g.exp[job]) {
+    // none of these tokens has an adapter, but others of their tile do
+    const int nch = (ttotal + g.per - 1) / g.per, w8 = g.width / 8;
+    for (int i = tid; i < 128 * nch * w8; i += kMultiThreads) {
+      const int q8 = i % w8, row = i / w8 / nch, c = i / w8 - row * nch;
+      if (row0 + row < g.M)
+        *reinterpret_cast<uint4*>(g.exp[job] + (((tile * g.cmax + c) * g.tn + (row0 + row - tok0)) * g.width + 8 * q8)) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
   }
   if (g.lazy) griddep_wait();
   __syncthreads();
@@ -636,9 +659,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
 // G[a][f][j] = sum over the sorted tokens p of adapter a of X[perm[p], f] P[p][j], with X = x
 // and P = v for dA, X = dY and P = u for dB, both in one launch. A CTA takes 128 features and
 // one slice of one adapter's tokens; 64 tokens a step: the TMA warp gathers their rows (four
-// rows per instruction, one instruction per lane) into an MN-major tile, the three parts of P
-// come as a K-major tile of 3 r16 rows, and three MMAs multiply X with them: the first part
-// into one accumulator, the other two, 2^-8 of it, into a second. As in the projections two
+// rows per instruction, one instruction per lane) into an MN-major tile, or, where they follow one
+// another as the tokens of a request or sample do, copies them in two boxes; the three parts of P
+// come as a K-major tile of 3 r16 rows, and two MMAs multiply X with them: the first two parts
+// into an accumulator each, the third, 2^-8 of the second, on top of the second's. As in the projections two
 // pairs of accumulators take turns of kFlushSteps steps and are added up in registers.
 // The work is bound by reading X once (it is often still in L2 from the projections); tokens
 // of other adapters are never read, so neither their number nor their values matter. An
@@ -646,6 +670,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
 // finish adds up in slice order.
 struct MultiGradArgs {
   CUtensorMap tmX[2];  // x [M, K], dY [M, N]: boxes of 1 x 64, for gathers
+  CUtensorMap tmR[2];  // the same in boxes of 64 x 64
   CUtensorMap tmP[2];  // parts of v, u: [3 r16][ldp] in boxes of 3 r16 x 64
   float* out[2];
   int64_t F[2];
@@ -685,6 +710,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
     s_abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&g.tmX[job]);
+    tma_prefetch_desc(&g.tmR[job]);
     tma_prefetch_desc(&g.tmP[job]);
   }
   if (warp == 1) {
@@ -710,6 +736,8 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
       for (int i = 0; i < sl.steps && all; ++i, p.next(nst)) {
         const int s = p.s;
         const int4 rows = *reinterpret_cast<const int4*>(g.perm + sl.p0 + i * 64 + (lane & 15) * 4);
+        const int row0 = __shfl_sync(0xffffffffu, rows.x, 0), mine0 = row0 + (lane & 15) * 4;
+        const bool run = __all_sync(0xffffffffu, rows.x == mine0 && rows.y == mine0 + 1 && rows.z == mine0 + 2 && rows.w == mine0 + 3);
         const bool ok = i < nst || wait_or_abort(&empty[s], p.ph ^ 1u, g.wait_ns, &s_abort, 96, true);
         all = __all_sync(0xffffffffu, ok);
         if (!all) break;
@@ -722,7 +750,10 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
         }
         __syncwarp();
         const int half = lane >> 4;
-        if (half == 0 || both)
+        if (run) {
+          if ((lane & 15) == 0 && (half == 0 || both))
+            tma_load_2d(st + half * 8192, &g.tmR[job], &full[s], static_cast<int32_t>(f0) + half * 64, row0);
+        } else if (half == 0 || both)
           tma_gather4(st + half * 8192 + (lane & 15) * 512, &g.tmX[job], &full[s],
                       static_cast<int32_t>(f0) + half * 64, rows);
         ++issued;
@@ -732,6 +763,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
     } else if (warp == 1) {
       if (lane == 0) {
         const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
+        const uint32_t idesc2 = idesc_bf16(128, static_cast<uint32_t>(2 * r16), 1u, 0u);
         const uint32_t pstep = (static_cast<uint32_t>(r16) * 128u) >> 4;  // descriptor units per part
         const uint64_t ad0 = smem_desc(smem_u32(base), 8192, 1024, kLayoutSW128);
         const uint64_t bd0 = smem_desc(smem_u32(base) + 16384, 16, 1024, kLayoutSW128);
@@ -752,8 +784,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t a = ad + (2048u >> 4) * kk;
             const uint32_t acc = (turn > 0 || kk > 0) ? 1u : 0u;
-            mma_ss(d, a, bd + 2u * kk, idesc, acc);
-            mma_ss(d + r16, a, bd + pstep + 2u * kk, idesc, acc);
+            mma_ss(d, a, bd + 2u * kk, idesc2, acc);
             mma_ss(d + r16, a, bd + 2 * pstep + 2u * kk, idesc, 1u);
           }
           mma_commit(&empty[s]);
