@@ -1169,7 +1169,7 @@ ProjPlan plan_proj(int64_t M, int64_t csteps, int jobs, int dmax, int per, int r
   auto batches = [&] { return (slots + p.sb - 1) / p.sb; };
   while (p.sb > per && tiles * p.slices * batches() < nsm) p.sb = std::max(per, p.sb / 2 / per * per);
   p.nz = static_cast<int>(std::min<int64_t>(batches(), std::max<int64_t>(1, 2 * nsm / (tiles * p.slices))));
-  while (p.tmem < static_cast<uint32_t>(2 * p.sb * r16)) p.tmem <<= 1;
+  while (p.tmem < 256 && p.tmem < static_cast<uint32_t>(2 * p.sb * r16)) p.tmem <<= 1;
   return p;
 }
 

@@ -46,7 +46,9 @@ QNF4_DEV void drain_ring(uint64_t* full, int issued, int nst, unsigned long long
 }
 
 // A position in a ring of n slots: its slot and phase, advanced without a division (one on the
-// MMA thread's path costs more than the step's MMAs).
+// MMA warp's path costs more than the step's MMAs). The MMA warps walk their loops with all lanes,
+// so that everything but the instructions of the one elected lane is uniform and stays in uniform
+// registers, where the MMAs want their descriptors.
 struct RingPos {
   int s = 0;
   uint32_t ph = 0;
@@ -84,8 +86,11 @@ struct RingPos {
 constexpr int kFlushSteps = 4;
 constexpr uint32_t kProjRing = 104u * 1024u;
 constexpr uint32_t kProjSmem = 1024u + kProjRing;  // two CTAs per SM
-constexpr int kProjMaxCols = 128;              // slots x r16 of a batch: two accumulators of 128 columns
-static_assert(3u * (16384u + kProjMaxCols * 128u) <= kProjRing, "three steps");
+// Slots x r16 of a batch. Up to 128 columns the two accumulators fit the CTA's half of TMEM; a
+// wider batch (rare with many tokens: more than two adapters of rank 64 among 128 of them) uses one
+// and waits for each flush, which costs less than streaming X again for a second batch.
+constexpr int kProjMaxCols = 256;
+static_assert(2u * (16384u + kProjMaxCols * 128u) <= kProjRing, "two steps");
 static_assert(128u * 68u * 4u + 128u * 64u * 4u <= kProjRing, "the sums reuse the rings");
 
 struct ProjArgs {
@@ -158,10 +163,10 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 
   const int r16 = g.r16;
   const uint32_t xbytes = static_cast<uint32_t>(g.xrows) * 128u;
-  const int per_slice = (g.nsteps[job] + g.slices - 1) / g.slices;
-  const int k0 = static_cast<int>(rank) * per_slice;
-  const int left = g.nsteps[job] - k0;
-  const int steps = left < 0 ? 0 : (left < per_slice ? left : per_slice);
+  // the slices take the steps in turn: a cluster's CTAs read neighbouring columns of the same rows
+  // at about the same time, so a DRAM page opened for a row serves all of them
+  const int k0 = static_cast<int>(rank);
+  const int steps = g.nsteps[job] > k0 ? (g.nsteps[job] - k0 + g.slices - 1) / g.slices : 0;
   // X of the first steps of the CTA's first batch (there may be none: then they are waited for
   // at the end)
   const uint32_t fmost = static_cast<uint32_t>(g.sb * r16) * 128u;
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < ahead; ++i) {
       mbar_expect_more(&full[i], xbytes);
-      tma_load_2d(base + i * xbytes, &g.tmX[job], &full[i], (k0 + i) * 64, static_cast<int32_t>(row0));
+      tma_load_2d(base + i * xbytes, &g.tmX[job], &full[i], (k0 + i * g.slices) * 64, static_cast<int32_t>(row0));
     }
   }
 
@@ -240,6 +245,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 
   for (int first = z * g.sb; first < total; first += g.nz * g.sb) {  // alike in the whole cluster
     const int nb = total - first < g.sb ? total - first : g.sb;
+    const bool two = 2 * nb * r16 <= static_cast<int>(g.tmem_cols);  // accumulators
     for (int w = tid; w < words; w += kMultiThreads) {
       int s = s_opre[w];
       for (uint32_t m = s_own[w]; m; m &= m - 1, ++s)
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
             all = __all_sync(0xffffffffu, wait_or_abort(&empty[s], pos.ph ^ 1u, g.wait_ns, &s_abort, 91, true));
             if (!all) break;
           }
-          const int32_t c = (k0 + i - it) * 64;
+          const int32_t c = (k0 + (i - it) * g.slices) * 64;
           const uint32_t fbytes = static_cast<uint32_t>(nb) * fslot;
           if (lane == 0) {
             if (i < ahead) {  // X is on its way
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0 && !s_abort) {
+      if (!__shfl_sync(0xffffffffu, s_abort, 0)) {
         const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(nb * r16), 0u, 0u);
         const uint64_t ad0 = smem_desc(smem_u32(base), 16, 1024, kLayoutSW128);
         const uint64_t bd0 = smem_desc(smem_u32(fring), 16, 1024, kLayoutSW128);
@@ -286,24 +292,29 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         uint32_t b = turn_n;
         for (int i = 0; i < steps && ok; ++i, pos.next(nst)) {
           const int s = pos.s, turn = i % kFlushSteps;
-          if (turn == 0 && b >= 2)
+          if (turn == 0 && two && b >= 2)
             ok = wait_or_abort(&acc_free[b & 1], (b / 2 - 1) & 1u, g.wait_ns, &s_abort, 90);
+          if (turn == 0 && !two && b >= 1)
+            ok = wait_or_abort(&acc_free[(b - 1) & 1], ((b - 1) / 2) & 1u, g.wait_ns, &s_abort, 90);
           ok = ok && wait_or_abort(&full[s], pos.ph, g.wait_ns, &s_abort, 93);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           // (rows past xrows are whatever lies there: their products are not read)
           const uint64_t ad = ad0 + ((static_cast<uint32_t>(s) * xbytes) >> 4);
           const uint64_t bd = bd0 + ((static_cast<uint32_t>(s) * fstage) >> 4);
-          const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2);
+          const uint32_t d = tmem + (two ? (b & 1u) * (g.tmem_cols / 2) : 0u);
+          const bool last = turn == kFlushSteps - 1 || i == steps - 1;
+          if (lane == 0) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ss(d, ad + 2u * kk, bd + 2u * kk, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&empty[s]);
-          if (turn == kFlushSteps - 1 || i == steps - 1) {
-            mma_commit(&acc_full[b & 1]);
-            ++b;
+            for (int kk = 0; kk < 4; ++kk) mma_ss(d, ad + 2u * kk, bd + 2u * kk, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&empty[s]);
+            if (last) mma_commit(&acc_full[b & 1]);
           }
+          __syncwarp();
+          b += last;
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
           mma_commit(&fin_bar);
           drain_wait(&fin_bar, 0, g.wait_ns, 95);
         }
@@ -324,7 +335,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         ok = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], (b / 2) & 1u, g.wait_ns, &s_abort, 94));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t d = tmem + (two ? (b & 1u) * (g.tmem_cols / 2) : 0u) + (static_cast<uint32_t>(q * 32) << 16);
         for (int sl = 0; sl < nb; ++sl) {
           if (!__any_sync(0xffffffffu, mine == sl)) continue;
 #pragma unroll
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
       if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 97);
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
+      {
         const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
         const uint32_t idesc2 = idesc_bf16(128, static_cast<uint32_t>(2 * r16), 1u, 0u);
         const uint32_t pstep = (static_cast<uint32_t>(r16) * 128u) >> 4;  // descriptor units per part
@@ -775,25 +786,28 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
           if (turn == 0 && b >= 2)
             ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 89);
           ok = ok && wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 98);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint32_t so = (static_cast<uint32_t>(s) * stage) >> 4;
           const uint64_t ad = ad0 + so, bd = bd0 + so;
           const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
+          const bool last = turn == kFlushSteps - 1 || i == sl.steps - 1;
+          if (lane == 0) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t a = ad + (2048u >> 4) * kk;
-            const uint32_t acc = (turn > 0 || kk > 0) ? 1u : 0u;
-            mma_ss(d, a, bd + 2u * kk, idesc2, acc);
-            mma_ss(d + r16, a, bd + 2 * pstep + 2u * kk, idesc, 1u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t a = ad + (2048u >> 4) * kk;
+              const uint32_t acc = (turn > 0 || kk > 0) ? 1u : 0u;
+              mma_ss(d, a, bd + 2u * kk, idesc2, acc);
+              mma_ss(d + r16, a, bd + 2 * pstep + 2u * kk, idesc, 1u);
+            }
+            mma_commit(&empty[s]);
+            if (last) mma_commit(&acc_full[b & 1]);
           }
-          mma_commit(&empty[s]);
-          if (turn == kFlushSteps - 1 || i == sl.steps - 1) {
-            mma_commit(&acc_full[b & 1]);
-            ++b;
-          }
+          __syncwarp();
+          b += last;
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
           mma_commit(&fin_bar);
           drain_wait(&fin_bar, 0, g.wait_ns, 100);
         }

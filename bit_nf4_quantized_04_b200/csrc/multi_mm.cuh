@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = idesc_bf16(256, 256, 0u, MN ? 1u : 0u);
       const uint32_t lay = g.rp == 16 ? 6u : (g.rp == 32 ? 4u : 2u);  // 32-, 64-, 128-byte swizzle
       const uint32_t rowb = 2u * static_cast<uint32_t>(g.rp);
@@ -342,31 +342,36 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
         tile_of(u, t, f);
         const int nx = g.cnt[t];
         if (k >= 2) ok = wait_or_abort(&acc_free[k & 1], static_cast<uint32_t>(k / 2 - 1) & 1u, g.wait_ns, &s_abort, 103);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(k & 1) * 256u;
         for (int i = 0; i < g.nk + nx; ++i, p.next(kMmStages)) {
           const int s = p.s;
-          ok = wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 104);
+          ok = __all_sync(0xffffffffu, wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 104));
           if (!ok) break;
           tc_fence_after();
           const uint32_t so = static_cast<uint32_t>(s) * (kMmStage >> 4);
           if (i < g.nk) {
             const uint64_t ad = ad0 + so, bd = bd0 + so;
+            if (lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t h = (kk >> 2) * (kMmHalf >> 4), k4 = kk & 3;
-              mma2_ss(d, ad + h + 2u * k4, bd + h + (MN ? (2048u >> 4) : 2u) * k4, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t h = (kk >> 2) * (kMmHalf >> 4), k4 = kk & 3;
+                mma2_ss(d, ad + h + 2u * k4, bd + h + (MN ? (2048u >> 4) : 2u) * k4, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+              }
+              mma2_commit(&empty[s]);
             }
-          } else {
+          } else if (lane == 0) {
             const uint64_t ad = ae0 + so, bd = be0 + so;
             for (int kk = 0; kk < g.rp / 16; ++kk) mma2_ss(d, ad + 2u * kk, bd + (MN ? (2048u >> 4) : 2u) * kk, idesc, 1u);
+            mma2_commit(&empty[s]);
           }
-          mma2_commit(&empty[s]);
+          __syncwarp();
         }
-        mma2_commit(&acc_full[k & 1]);
+        if (lane == 0) mma2_commit(&acc_full[k & 1]);
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         mma2_commit(&fin_bar);
         drain_wait(&fin_bar, 0, g.wait_ns, 105);
       }
