@@ -472,8 +472,24 @@ def multi_workspace_size(op: int, N: int, K: int, M: int, n: int, r: int) -> int
     return int(lib.qnf4_multi_workspace_size(op, N, K, M, n, r))
 
 
+_BF16 = torch.bfloat16
+
+
 def _multi_args(N: int, K: int, x, ids, A, B, scales, dY=None):
-    """Checks of a many-adapter call's tensors against one another: (M, n, r)."""
+    """Checks of a many-adapter call's tensors against one another: (M, n, r). One pass over the
+    properties a right call has; only a wrong one is looked at again for what to say."""
+    d = x.get_device()
+    if (x.dim() == 2 and A.dim() == 3 and B.dim() == 3 and x.dtype is _BF16 and A.dtype is _BF16 and B.dtype is _BF16
+            and ids.dtype is torch.int32 and scales.dtype is torch.float32 and ids.dim() == 1 and scales.dim() == 1):
+        M, n, r = x.size(0), A.size(0), A.size(1)
+        if (x.size(1) == K and A.size(2) == K and B.size(0) == n and B.size(1) == N and B.size(2) == r
+                and ids.size(0) == M and scales.size(0) == n
+                and d >= 0 and A.get_device() == d and B.get_device() == d and ids.get_device() == d
+                and scales.get_device() == d and x.is_contiguous() and A.is_contiguous() and B.is_contiguous()
+                and ids.is_contiguous() and scales.is_contiguous()
+                and (dY is None or (dY.dtype is _BF16 and dY.dim() == 2 and dY.size(0) == M and dY.size(1) == N
+                                    and dY.get_device() == d and dY.is_contiguous()))):
+            return M, n, r
     for t, nm in ((x, "x"), (A, "A"), (B, "B")):
         _req(t, torch.bfloat16, nm)
     _req(ids, torch.int32, "ids")
@@ -492,11 +508,7 @@ def _multi_args(N: int, K: int, x, ids, A, B, scales, dY=None):
         raise ValueError(f"scales must be [{n}], got {tuple(scales.shape)}")
     if dY is not None and tuple(_req(dY, torch.bfloat16, "dY").shape) != (M, N):
         raise ValueError(f"dY must be [{M}, {N}], got {tuple(dY.shape)}")
-    d = x.get_device()
-    for t in (ids, A, B, scales) if dY is None else (ids, A, B, scales, dY):
-        if t.get_device() != d:
-            raise ValueError("all tensors must be on one device")
-    return M, n, r
+    raise ValueError("all tensors must be on one device")
 
 
 def _multi_out(t, shape, dtype, name: str, like):
@@ -509,8 +521,9 @@ def _multi_out(t, shape, dtype, name: str, like):
 
 def _multi_ws(need: int, like: torch.Tensor, ws):
     """(pointer owner, its bytes) of the caller's workspace, or of a new one."""
-    if ws is None:
-        return like.new_empty(need, dtype=torch.uint8), need
+    if ws is None:  # (elements of the tensor's own type: one keyword less to parse per call)
+        es = like.element_size()
+        return like.new_empty((need + es - 1) // es), need
     _ws(need, like, ws)
     if ws.get_device() != like.get_device():
         raise ValueError("the workspace must be on the tensors' device")
@@ -519,7 +532,7 @@ def _multi_ws(need: int, like: torch.Tensor, ws):
 
 def _multi_fwd(fn: str, base, N, K, x, ids, A, B, scales, h, ws):
     M, n, r = _multi_args(N, K, x, ids, A, B, scales)
-    h = _multi_out(h, (M, N), torch.bfloat16, "h", x)
+    h = x.new_empty((M, N)) if h is None else _multi_out(h, (M, N), torch.bfloat16, "h", x)
     if M == 0:
         return h
     with _on(x):

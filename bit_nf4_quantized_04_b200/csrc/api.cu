@@ -1613,10 +1613,18 @@ qnf4_status check_multi_args(int64_t N, int64_t K, int64_t M, int n, int r, bool
 // ---------------------------------------------------------------------------
 // Gradient norms and clipping over a list of tensors (see grad.cuh)
 // ---------------------------------------------------------------------------
+// Elements of a piece of this list.
+int grad_piece_size(int32_t count, const int64_t* elems) {
+  int64_t total = 0;
+  for (int32_t t = 0; t < count; ++t) total += elems[t];
+  return total <= kGradShortList ? kGradShortPiece : kGradPiece;
+}
+
 // Pieces of one adapter's part over the whole list.
 int64_t grad_pieces(int32_t count, const int64_t* elems, int32_t n) {
+  const int piece = grad_piece_size(count, elems);
   int64_t p = 0;
-  for (int32_t t = 0; t < count; ++t) p += (elems[t] / n + kGradPiece - 1) / kGradPiece;
+  for (int32_t t = 0; t < count; ++t) p += (elems[t] / n + piece - 1) / piece;
   return p;
 }
 
@@ -1649,8 +1657,9 @@ qnf4_status check_grad_args(int32_t count, const void* const* g, const int32_t* 
 // The launches' table of tensors [t0, t0 + count).
 template <int CAP>
 void grad_tab(GradTab<CAP>* tab, int32_t t0, int32_t count, const void* const* g, const int32_t* dtype,
-              const int64_t* elems, int32_t n, void* const* out, int64_t base, int64_t pieces) {
+              const int64_t* elems, int32_t n, void* const* out, int piece, int64_t base, int64_t pieces) {
   std::memset(tab->bf16, 0, sizeof(tab->bf16));
+  tab->piece = piece;
   tab->count = count;
   tab->n = n;
   tab->base = base;
@@ -1661,7 +1670,7 @@ void grad_tab(GradTab<CAP>* tab, int32_t t0, int32_t count, const void* const* g
     tab->in[i] = g[t];
     tab->out[i] = out ? out[t] : nullptr;
     tab->part[i] = elems[t] / n;
-    tab->piece0[i + 1] = tab->piece0[i] + (tab->part[i] + kGradPiece - 1) / kGradPiece;
+    tab->piece0[i + 1] = tab->piece0[i] + (tab->part[i] + piece - 1) / piece;
     if (dtype[t] == QNF4_OUT_BF16) tab->bf16[i >> 5] |= 1u << (i & 31);
   }
 }
@@ -1679,26 +1688,33 @@ qnf4_status grad_norm_clip_in(int32_t count, const void* const* g, const int32_t
                                          align256(static_cast<size_t>(pieces) * n * sizeof(double)));
   static thread_local GradTab<CAP> tab;  // up to 16 KB: kept off the stack
   int launches = 0;
+  const int piece = grad_piece_size(count, elems);
+  // (a list cut over several launches would have its norms added up in each)
+  const bool few = grad_few(pieces, n) && count <= CAP;
   auto pass = [&](bool scale) {
     int64_t base = 0;
     for (int32_t t0 = 0; t0 < count; t0 += CAP) {
-      grad_tab<CAP>(&tab, t0, std::min(CAP, count - t0), g, dtype, elems, n, out, base, pieces);
+      grad_tab<CAP>(&tab, t0, std::min(CAP, count - t0), g, dtype, elems, n, out, piece, base, pieces);
       const int64_t per = tab.piece0[tab.count];
       base += per;
       if (per == 0) continue;
       const int64_t ctas = (per * n + kGradWarps - 1) / kGradWarps;
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ctas, num_sms() * 8)));
       if (scale)
-        launch_pdl(k_grad_scale<CAP>, grid, dim3(32 * kGradWarps), 0, s, tab, static_cast<const float*>(coef));
+        launch_pdl(k_grad_scale<CAP>, grid, dim3(32 * kGradWarps), 0, s, tab,
+                   few ? static_cast<const float*>(nullptr) : static_cast<const float*>(coef),
+                   static_cast<const double*>(sums), max_norm, norm);
       else
         launch_pdl(k_grad_sq<CAP>, grid, dim3(32 * kGradWarps), 0, s, tab, sums);
       ++launches;
     }
   };
   pass(false);
-  launch_pdl(k_grad_norm, dim3(static_cast<unsigned>(n)), dim3(512), 0, s, static_cast<const double*>(sums),
-             pieces, max_norm, norm, out ? coef : static_cast<float*>(nullptr));
-  ++launches;
+  if (!out || !few || pieces == 0) {
+    launch_pdl(k_grad_norm, dim3(static_cast<unsigned>(n)), dim3(512), 0, s, static_cast<const double*>(sums),
+               pieces, max_norm, few ? 1 : 0, norm, out && !few ? coef : static_cast<float*>(nullptr));
+    ++launches;
+  }
   if (out) pass(true);
   return launched(out ? "clip_grad_norm" : "grad_norm", launches);
 }

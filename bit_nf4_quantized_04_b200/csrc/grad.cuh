@@ -23,7 +23,11 @@ namespace qnf4 {
 constexpr int kGradMaxTensors = 512;
 constexpr int kGradFewTensors = 32;
 constexpr int kGradWarps = 8;
-constexpr int kGradPiece = 4096;      // elements of a piece
+// Elements of a piece: 4096, or 1024 where the whole list is short, so that there are more warps
+// than SMs can hide latency with (14 bf16 gradients, 2.5 M elements: 610 warps against 2440).
+constexpr int kGradPiece = 4096;
+constexpr int kGradShortPiece = 1024;
+constexpr int64_t kGradShortList = 1 << 23;  // elements
 
 template <int CAP>
 struct GradTab {
@@ -32,6 +36,7 @@ struct GradTab {
   int64_t part[CAP];           // elements of one adapter's part
   int64_t piece0[CAP + 1];     // pieces per adapter before tensor t (in this launch)
   uint32_t bf16[CAP / 32];     // bit t: tensor t is bf16, else fp32
+  int piece;                               // elements of a piece
   int count;                               // tensors in this launch
   int n;                                   // adapters
   int64_t base;                            // pieces per adapter in earlier launches
@@ -53,8 +58,8 @@ QNF4_DEV GradPiece grad_piece(const GradTab<CAP>& g, int64_t q) {
   }
   GradPiece p;
   p.t = lo;
-  p.e0 = (q - g.piece0[lo]) * kGradPiece;
-  p.e1 = p.e0 + kGradPiece < g.part[lo] ? p.e0 + kGradPiece : g.part[lo];
+  p.e0 = (q - g.piece0[lo]) * g.piece;
+  p.e1 = p.e0 + g.piece < g.part[lo] ? p.e0 + g.piece : g.part[lo];
   return p;
 }
 
@@ -90,7 +95,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) k_grad_sq(const __grid_consta
       const int64_t h = head_elems(x, len), nv = (len - h) / 8;
       const uint4* xv = reinterpret_cast<const uint4*>(x + h);
       if (lane < h) s0 = sq_add(s0, bf16_of(x[lane]));
-#pragma unroll 4
+#pragma unroll 8
       for (int64_t i = lane; i < nv; i += 32) {
         const uint4 v = __ldg(xv + i);
         s0 = sq_add(sq_add(s0, bf16lo(v.x)), bf16hi(v.x));
@@ -121,15 +126,41 @@ __global__ void __launch_bounds__(32 * kGradWarps) k_grad_sq(const __grid_consta
   }
 }
 
-// norm[a] and, for clipping, coef[a] = min(1, max_norm / (norm[a] + 1e-6)); a NaN norm gives
-// a NaN factor. One CTA per adapter, its pieces added in a fixed order.
+// The sum of an adapter's pieces by one warp, in a fixed order (all lanes return it).
+QNF4_DEV double grad_warp_sum(const double* src, int64_t pieces) {
+  double s = 0.0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x & 31; i < pieces; i += 32) s += __ldcg(src + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+// min(1, max_norm / (norm + 1e-6)); a NaN norm gives a NaN factor
+QNF4_DEV float grad_factor(float norm, float max_norm) {
+  const float c = max_norm / (norm + 1e-6f);
+  return c > 1.f ? 1.f : c;
+}
+
+// Lists of few pieces need no kernel of their own for the norms: every CTA of the scaling kernel
+// adds them up itself.
+constexpr int64_t kGradFewPieces = 4096;  // of all adapters together
+constexpr int kGradFewAdapters = 64;
+inline bool grad_few(int64_t pieces, int n) { return pieces * n <= kGradFewPieces && n <= kGradFewAdapters; }
+
+// norm[a] and, for clipping, the factor coef[a]. One CTA per adapter, its pieces added in a fixed
+// order (few pieces: in the order of the scaling kernel).
 __global__ void __launch_bounds__(512) k_grad_norm(const double* __restrict__ part_sum, int64_t pieces,
-                                                   float max_norm, float* __restrict__ norm,
+                                                   float max_norm, int few, float* __restrict__ norm,
                                                    float* __restrict__ coef) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ double s_sum[16];
   const double* src = part_sum + blockIdx.x * pieces;
+  if (few) {
+    const double t = threadIdx.x < 32 ? grad_warp_sum(src, pieces) : 0.0;
+    if (threadIdx.x == 0) norm[blockIdx.x] = static_cast<float>(sqrt(t));
+    return;
+  }
   double s = 0.0;
 #pragma unroll 8
   for (int64_t i = threadIdx.x; i < pieces; i += 512) s += __ldcg(src + i);
@@ -142,27 +173,37 @@ __global__ void __launch_bounds__(512) k_grad_norm(const double* __restrict__ pa
     for (int i = 0; i < 16; ++i) t += s_sum[i];
     const float v = static_cast<float>(sqrt(t));
     norm[blockIdx.x] = v;
-    if (coef) {
-      const float c = max_norm / (v + 1e-6f);
-      coef[blockIdx.x] = c > 1.f ? 1.f : c;
-    }
+    if (coef) coef[blockIdx.x] = grad_factor(v, max_norm);
   }
 }
 
-// out = g * coef[a]; where the output is the input, an adapter whose factor is 1 is left.
+// out = g * coef[a] (coef null: few pieces, added up here, and written to norm by CTA 0); where the output is the input, an adapter whose factor is 1 is left.
 template <int CAP>
 __global__ void __launch_bounds__(32 * kGradWarps) k_grad_scale(const __grid_constant__ GradTab<CAP> g,
-                                                               const float* __restrict__ coef) {
+                                                               const float* __restrict__ coef,
+                                                               const double* __restrict__ part_sum,
+                                                               float max_norm, float* __restrict__ norm) {
   griddep_wait();
   griddep_launch_dependents();
+  __shared__ float s_coef[kGradFewAdapters];
   const int lane = threadIdx.x & 31;
+  if (!coef) {
+    for (int a = threadIdx.x >> 5; a < g.n; a += kGradWarps) {
+      const float v = static_cast<float>(sqrt(grad_warp_sum(part_sum + a * g.pieces, g.pieces)));
+      if (lane == 0) {
+        s_coef[a] = grad_factor(v, max_norm);
+        if (blockIdx.x == 0) norm[a] = v;
+      }
+    }
+    __syncthreads();
+  }
   const int64_t per = g.piece0[g.count];
   const int64_t total = per * g.n;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5); w < total;
        w += static_cast<int64_t>(gridDim.x) * kGradWarps) {
     const int64_t a = w / per, q = w - a * per;
     const GradPiece p = grad_piece(g, q);
-    const float c = __ldcg(coef + a);
+    const float c = coef ? __ldcg(coef + a) : s_coef[a];
     if (c == 1.f && g.out[p.t] == g.in[p.t]) continue;
     const int64_t at = a * g.part[p.t] + p.e0, len = p.e1 - p.e0;
     if (grad_is_bf16(g, p.t)) {
@@ -174,7 +215,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) k_grad_scale(const __grid_con
       uint4* yv = reinterpret_cast<uint4*>(y + h);
       auto one = [&](int64_t i) { y[i] = static_cast<uint16_t>(pack_bf16x2(bf16_of(x[i]) * c, 0.f)); };
       if (lane < h) one(lane);
-#pragma unroll 4
+#pragma unroll 8
       for (int64_t i = lane; i < nv; i += 32) {
         uint4 v = xv[i];
         v.x = pack_bf16x2(bf16lo(v.x) * c, bf16hi(v.x) * c);
