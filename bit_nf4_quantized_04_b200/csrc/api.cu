@@ -1148,7 +1148,9 @@ struct MultiPlan {
 // Product for many tokens (multi_mm.cuh) or k_gemm's? The former costs writing the base in 16
 // bits and tiles of 256 tokens; its output rows must be 16-byte aligned, and its copies of the
 // adapters stay below the base's size.
-constexpr int64_t kMmMinTokens = 192;
+// (measured, 8 adapters of r = 16 through 4096 x 4096, k_gemm against this: forward NF4 43 / 52 us at
+// 512 tokens, 54 / 53 at 1024; bf16 41 / 44, 50 / 45; backward NF4 68 / 72, 86 / 75)
+constexpr int64_t kMmMinTokens = 768;
 bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
   return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K);
 }
@@ -1550,7 +1552,9 @@ qnf4_status multi_grad(const MultiPlan& P, const Adapters& ad, const void* x, co
   g.part_elems = P.part_elems;
   g.ctr_elems = P.ctr_elems;
   g.wait_ns = g_wait_ns;
-  launch_multi_kernel(k_multi_grad, g_grad_smem_set, dim3(P.ftiles, P.slmax), kMultiThreads, kGradRing + 1024, 1, s, g);
+  // two CTAs per SM at once; with few slices one each
+  const int64_t gy = std::max<int64_t>(1, std::min<int64_t>(P.slmax, 2 * num_sms() / P.ftiles));
+  launch_multi_kernel(k_multi_grad, g_grad_smem_set, dim3(P.ftiles, static_cast<unsigned>(gy)), kMultiThreads, kGradRing + 1024, 1, s, g);
   return launched("multi_grad");
 }
 

@@ -885,14 +885,14 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       }
     };
     // MULTI, dense sources: the chunks of unit w through the ext tile, one at a time (each
-    // waits until the MMAs of the one before, counted over all units, have read it;
-    // converter set 0 only).
+    // waits until the MMAs of the one before, counted over all units, have read it, with its
+    // own words already in registers; converter set 0 only).
     int kw = 0;
     auto write_ext_multi = [&](const Unit& w, int k) {
       for (int x = 0; x < w.nx; ++x, ++kw) {
-        if (kw > 0 && !wait_or_abort(&ext_free, (kw - 1) & 1, g.wait_ns, &s_abort, 36)) return;
         uint32_t v[32];
         ext_words(w, w.x0 + x, t, k, v);
+        if (kw > 0 && !wait_or_abort(&ext_free, (kw - 1) & 1, g.wait_ns, &s_abort, 36)) return;
         store_row_sw128(base + sp.ext, t, v);
         fence_proxy_async();
         mbar_arrive(&ext_bar);

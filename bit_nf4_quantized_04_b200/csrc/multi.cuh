@@ -648,6 +648,11 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
   uint16_t* sm = reinterpret_cast<uint16_t*>(prep_sm);  // [64][r + 1]
   for (int64_t u = blockIdx.x - 1; u < nt * g.n; u += gridDim.x - 1) {
     const int64_t a = u / nt, n0 = (u - a * nt) * 64;
+    if (g.M <= 4 * kPrepThreads) {  // few tokens: is there one that names this adapter?
+      bool named = false;
+      for (int64_t m = tid; m < g.M; m += kPrepThreads) named |= g.ids[m] == static_cast<int>(a);
+      if (!__syncthreads_or(named)) continue;
+    }
     const int rows = static_cast<int>(g.N - n0 < 64 ? g.N - n0 : 64);
     const uint16_t* src = g.B + (a * g.N + n0) * g.r;
     for (int i = tid; i < rows * g.r; i += kPrepThreads) sm[(i / g.r) * (g.r + 1) + i % g.r] = src[i];
@@ -669,7 +674,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
 // ---------------------------------------------------------------------------
 // G[a][f][j] = sum over the sorted tokens p of adapter a of X[perm[p], f] P[p][j], with X = x
 // and P = v for dA, X = dY and P = u for dB, both in one launch. A CTA takes 128 features and
-// one slice of one adapter's tokens; 64 tokens a step: the TMA warp gathers their rows (four
+// the slices blockIdx.y, blockIdx.y + gridDim.y, ... of the adapters' tokens, with the loads of the
+// next slice on their way while one is written out (many adapters of a few tokens each make short
+// slices, and a CTA for each spent its time on setting up); 64 tokens a step: the TMA warp gathers their rows (four
 // rows per instruction, one instruction per lane) into an MN-major tile, or, where they follow one
 // another as the tokens of a request or sample do, copies them in two boxes; the three parts of P
 // come as a K-major tile of 3 r16 rows, and two MMAs multiply X with them: the first two parts
@@ -703,7 +710,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
   __shared__ __align__(8) uint64_t full[kMultiMaxStages], empty[kMultiMaxStages], acc_full[2], acc_free[2], fin_bar;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_last;
+  __shared__ volatile int s_last;
   uint8_t* base = gsm_raw + ((1024u - (smem_u32(gsm_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int job = static_cast<int>(blockIdx.x) < g.ft[0] ? 0 : 1;
@@ -734,22 +741,23 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
   const uint32_t tmem = s_tmem;
   griddep_wait();
   griddep_launch_dependents();
-  if (static_cast<int>(blockIdx.y) < *g.nslices) {
-    const GradSlice sl = g.slices[blockIdx.y];
-    const int r16 = g.r16;
-    const uint32_t stage = 16384u + static_cast<uint32_t>(3 * r16) * 128u;
-    const int fit = static_cast<int>(g.ring_bytes / stage);
-    const int nst = fit < kMultiMaxStages ? fit : kMultiMaxStages;
-    if (warp == 0) {
-      int issued = 0;
-      bool all = true;
-      RingPos p;  // (the phase of a slot's previous use is the opposite one)
+  const int nsl = *g.nslices;
+  const int r16 = g.r16;
+  const uint32_t stage = 16384u + static_cast<uint32_t>(3 * r16) * 128u;
+  const int fit = static_cast<int>(g.ring_bytes / stage);
+  const int nst = fit < kMultiMaxStages ? fit : kMultiMaxStages;
+  if (warp == 0) {
+    int issued = 0;
+    bool all = true;
+    RingPos p;  // (the phase of a slot's previous use is the opposite one)
+    for (int y = blockIdx.y; y < nsl && all; y += gridDim.y) {
+      const GradSlice sl = g.slices[y];
       for (int i = 0; i < sl.steps && all; ++i, p.next(nst)) {
         const int s = p.s;
         const int4 rows = *reinterpret_cast<const int4*>(g.perm + sl.p0 + i * 64 + (lane & 15) * 4);
         const int row0 = __shfl_sync(0xffffffffu, rows.x, 0), mine0 = row0 + (lane & 15) * 4;
         const bool run = __all_sync(0xffffffffu, rows.x == mine0 && rows.y == mine0 + 1 && rows.z == mine0 + 2 && rows.w == mine0 + 3);
-        const bool ok = i < nst || wait_or_abort(&empty[s], p.ph ^ 1u, g.wait_ns, &s_abort, 96, true);
+        const bool ok = issued < nst || wait_or_abort(&empty[s], p.ph ^ 1u, g.wait_ns, &s_abort, 96, true);
         all = __all_sync(0xffffffffu, ok);
         if (!all) break;
         uint8_t* st = base + static_cast<uint32_t>(s) * stage;
@@ -769,62 +777,70 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
                       static_cast<int32_t>(f0) + half * 64, rows);
         ++issued;
       }
-      if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 97);
-      __syncwarp();
-    } else if (warp == 1) {
-      {
-        const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
-        const uint32_t idesc2 = idesc_bf16(128, static_cast<uint32_t>(2 * r16), 1u, 0u);
-        const uint32_t pstep = (static_cast<uint32_t>(r16) * 128u) >> 4;  // descriptor units per part
-        const uint64_t ad0 = smem_desc(smem_u32(base), 8192, 1024, kLayoutSW128);
-        const uint64_t bd0 = smem_desc(smem_u32(base) + 16384, 16, 1024, kLayoutSW128);
-        bool ok = true;
-        int b = 0;
-        RingPos p;
-        for (int i = 0; i < sl.steps && ok; ++i, p.next(nst)) {
-          const int s = p.s, turn = i % kFlushSteps;
-          if (turn == 0 && b >= 2)
-            ok = wait_or_abort(&acc_free[b & 1], static_cast<uint32_t>(b / 2 - 1) & 1u, g.wait_ns, &s_abort, 89);
-          ok = ok && wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 98);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t so = (static_cast<uint32_t>(s) * stage) >> 4;
-          const uint64_t ad = ad0 + so, bd = bd0 + so;
-          const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2);
-          const bool last = turn == kFlushSteps - 1 || i == sl.steps - 1;
-          if (lane == 0) {
+    }
+    if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 97);
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
+    const uint32_t idesc2 = idesc_bf16(128, static_cast<uint32_t>(2 * r16), 1u, 0u);
+    const uint32_t pstep = (static_cast<uint32_t>(r16) * 128u) >> 4;  // descriptor units per part
+    const uint64_t ad0 = smem_desc(smem_u32(base), 8192, 1024, kLayoutSW128);
+    const uint64_t bd0 = smem_desc(smem_u32(base) + 16384, 16, 1024, kLayoutSW128);
+    bool ok = true;
+    uint32_t b = 0;
+    RingPos p;
+    for (int y = blockIdx.y; y < nsl && ok; y += gridDim.y) {
+      const int steps = g.slices[y].steps;
+      for (int i = 0; i < steps && ok; ++i, p.next(nst)) {
+        const int s = p.s, turn = i % kFlushSteps;
+        if (turn == 0 && b >= 2)
+          ok = wait_or_abort(&acc_free[b & 1], (b / 2 - 1) & 1u, g.wait_ns, &s_abort, 89);
+        ok = ok && wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 98);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t so = (static_cast<uint32_t>(s) * stage) >> 4;
+        const uint64_t ad = ad0 + so, bd = bd0 + so;
+        const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2);
+        const bool last = turn == kFlushSteps - 1 || i == steps - 1;
+        if (lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = ad + (2048u >> 4) * kk;
-              const uint32_t acc = (turn > 0 || kk > 0) ? 1u : 0u;
-              mma_ss(d, a, bd + 2u * kk, idesc2, acc);
-              mma_ss(d + r16, a, bd + 2 * pstep + 2u * kk, idesc, 1u);
-            }
-            mma_commit(&empty[s]);
-            if (last) mma_commit(&acc_full[b & 1]);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t a = ad + (2048u >> 4) * kk;
+            const uint32_t acc = (turn > 0 || kk > 0) ? 1u : 0u;
+            mma_ss(d, a, bd + 2u * kk, idesc2, acc);
+            mma_ss(d + r16, a, bd + 2 * pstep + 2u * kk, idesc, 1u);
           }
-          __syncwarp();
-          b += last;
+          mma_commit(&empty[s]);
+          if (last) mma_commit(&acc_full[b & 1]);
         }
-        if (!ok && lane == 0) {
-          mma_commit(&fin_bar);
-          drain_wait(&fin_bar, 0, g.wait_ns, 100);
-        }
+        __syncwarp();
+        b += last;
       }
-      __syncwarp();
-    } else {
-      const int q = warp & 3, row = q * 32 + lane;
+    }
+    if (!ok && lane == 0) {
+      mma_commit(&fin_bar);
+      drain_wait(&fin_bar, 0, g.wait_ns, 100);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, row = q * 32 + lane;
+    const int64_t f = f0 + row;
+    const int64_t js = g.js[job];
+    const bool in = f < g.F[job];
+    const int64_t tiles = g.ft[0] + g.ft[1];
+    const int64_t tsz = static_cast<int64_t>(r16) * 128;
+    uint32_t b = 0;
+    for (int y = blockIdx.y; y < nsl; y += gridDim.y) {
+      const GradSlice sl = g.slices[y];
       float sum[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) sum[c] = 0.f;
       const int turns = (sl.steps + kFlushSteps - 1) / kFlushSteps;
-      bool fine = true;
-      for (int b = 0; b < turns && fine; ++b) {
-        fine = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], static_cast<uint32_t>(b / 2) & 1u, g.wait_ns, &s_abort, 99));
-        if (!fine) break;
+      for (int k = 0; k < turns; ++k, ++b) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], (b / 2) & 1u, g.wait_ns, &s_abort, 99))) break;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(b & 1) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t d = tmem + (b & 1u) * (g.tmem_cols / 2) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c * 16 < r16) {
@@ -839,20 +855,19 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
         tc_fence_before();
         mbar_arrive(&acc_free[b & 1]);
       }
+      // the four warps go on or give up together
       named_sync(1, 128);
-      const bool ok = !s_abort;
+      if (tid == 64) s_last = s_abort ? 0 : 1;
       named_sync(1, 128);
-      const int64_t f = f0 + row;
+      const bool ok = s_last != 0;
+      named_sync(1, 128);
+      if (!ok) break;
       float* out = g.out[job] + sl.a * g.as[job] + f * g.fs[job];
-      const int64_t js = g.js[job];
-      const bool in = f < g.F[job];
-      const int64_t tiles = g.ft[0] + g.ft[1];
-      const int64_t tsz = static_cast<int64_t>(r16) * 128;
-      const bool several = sl.count > 1;
-      bool write = ok && !several;
-      if (several) {
-        float* mine = g.part + ((sl.part0 + sl.index) * tiles + blockIdx.x) * tsz + row;
-        if (ok && in_bounds(((sl.part0 + sl.index) * tiles + blockIdx.x + 1) * tsz <= g.part_elems, 95)) {
+      bool write = true;
+      if (sl.count > 1) {
+        const int64_t at = (sl.part0 + sl.index) * tiles + blockIdx.x;
+        float* mine = g.part + at * tsz + row;
+        if (in_bounds((at + 1) * tsz <= g.part_elems, 95)) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c < r16) __stcg(mine + c * 128, sum[c]);
@@ -860,10 +875,8 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
         __threadfence();
         named_sync(1, 128);
         if (tid == 64) {
-          s_last = 0;
           const int64_t c = sl.group * tiles + blockIdx.x;
-          if (ok && in_bounds(c < g.ctr_elems, 96))
-            s_last = atomicAdd(g.ctr + c, 1u) == static_cast<unsigned>(sl.count - 1);
+          s_last = in_bounds(c < g.ctr_elems, 96) && atomicAdd(g.ctr + c, 1u) == static_cast<unsigned>(sl.count - 1);
         }
         named_sync(1, 128);
         write = s_last != 0;
@@ -878,6 +891,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
               if (c < r16) sum[c] += __ldcg(all + k * tiles * tsz + c * 128);
           }
         }
+        named_sync(1, 128);  // s_last is free again
       }
       if (write && in) {
         if (js == 1 && (g.r & 3) == 0) {
