@@ -1391,6 +1391,7 @@ qnf4_status multi_main(const BaseSrc& src, int main_src, const MultiPlan& P, con
   g.stage = stage_map(&mo, out, rows, M, rows) ? 1 : 0;
   g.part = reinterpret_cast<float*>(w8 + P.off_part);
   g.counters = reinterpret_cast<unsigned*>(w8 + P.off_ctr);
+  g.lazy_dep = P.main.units == P.main.grid ? 1 : 0;  // one unit per CTA: the base need not wait
   if (g_ev_start) cudaEventRecord(g_ev_start, s);
   const qnf4_status st = launch_multi(P.main, ma, mb, mbx, mo, none, g, s);
   if (g_ev_stop) cudaEventRecord(g_ev_stop, s);

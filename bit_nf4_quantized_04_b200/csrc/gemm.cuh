@@ -157,7 +157,8 @@ struct GemmArgs {
   int clus;               // > 1: no whole waves, and a tile's slices are the CTAs of a cluster
   int lazy_dep;           // programmatic dependent launch: 0 = every thread waits for the
                           // previous grid after the prologue; 1 = only the adapter chunk's
-                          // copy waits (its operand is the one the previous grid writes)
+                          // copy waits (its operand is the one the previous grid writes);
+                          // MULTI: each role waits after its base steps (one unit per CTA)
 };
 
 struct SmemPlan {
@@ -380,6 +381,13 @@ struct Unit {
   int ct, x0, nx;      // MULTI: column tile, first adapter chunk of this slice and their number
 };
 
+// MULTI: the adapter chunks of unit w's tile, dealt to its slices.
+QNF4_DEV void unit_chunks(const GemmArgs& g, Unit& w) {
+  const int chunks = (g.mt_cnt[w.ct] + g.mt_per - 1) / g.mt_per;
+  w.x0 = chunks * w.z / w.splits;
+  w.nx = chunks * (w.z + 1) / w.splits - w.x0;
+}
+
 template <bool MULTI = false>
 QNF4_DEV Unit unit_of(const GemmArgs& g, int u) {
   Unit w;
@@ -408,10 +416,8 @@ QNF4_DEV Unit unit_of(const GemmArgs& g, int u) {
   w.ext = g.has_ext && w.z == 0;
   w.ct = t / g.row_tiles;
   w.x0 = w.nx = 0;
-  if (MULTI) {  // the tile's adapter chunks, dealt to its slices
-    const int chunks = (g.mt_cnt[w.ct] + g.mt_per - 1) / g.mt_per;
-    w.x0 = chunks * w.z / w.splits;
-    w.nx = chunks * (w.z + 1) / w.splits - w.x0;
+  if (MULTI) {
+    if (!g.lazy_dep) unit_chunks(g, w);
   } else {
     w.nx = w.ext ? 1 : 0;
   }
@@ -602,8 +608,8 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       if (src_packed_tma(ASRC)) bytes += kPTile;
       if (src_table_tma(ASRC)) bytes += kTTile;
       for (int u = u0; u < g.nunits && ok; u += ustep) {
-        const Unit w = unit_of<MULTI>(g, u);
-        const int nload = w.nst + w.nx;
+        Unit w = unit_of<MULTI>(g, u);
+        int nload = w.nst + w.nx;
         int32_t kc = w.step0 * kStep;
         for (int i = 0; i < nload; ++i) {
           if (!mbar_try_wait(&empty1[s], ph ^ 1) &&
@@ -626,8 +632,13 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
             // the tables of this step's 64 contraction rows
             if (ASRC == A_CHANQ_MN) tma_load_2d(slot + sp.off_t1, &tmT, fb, 0, kc);
             tma_load_2d(slot + sp.off_b1, &tmB, fb, kc, (int32_t)w.col0);
+            if (MULTI && g.lazy_dep && i == w.nst - 1) {  // the base is on its way
+              griddep_wait();
+              unit_chunks(g, w);
+              nload += w.nx;
+            }
           } else {
-            if (g.lazy_dep && !dep) {
+            if (!MULTI && g.lazy_dep && !dep) {
               griddep_wait();
               dep = true;
             }
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       uint32_t ph = 0, ph2 = 0;
       int k = 0, kx = 0;  // units done, adapter chunks done
       for (int u = u0; u < g.nunits; u += ustep, ++k) {
-        const Unit w = unit_of<MULTI>(g, u);
+        Unit w = unit_of<MULTI>(g, u);
         // the previous unit's epilogue must have read the accumulator
         if (k > 0) {
           if (!wait_or_abort(&acc_empty, (k - 1) & 1, g.wait_ns, &s_abort, 26, true)) {
@@ -689,7 +700,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           tc_fence_after();
         }
         // (MULTI, dequantizing sources: the adapter chunks are ordinary steps of the A ring)
-        const int nmma = MULTI && DEQ ? w.nst + w.nx : w.nst;
+        int nmma = MULTI && DEQ ? w.nst + w.nx : w.nst;
         for (int i = 0; i < nmma; ++i) {
           uint64_t* bar = DEQ ? &full2[s2] : &full1[s];
           const uint32_t pp = DEQ ? ph2 : ph;
@@ -716,6 +727,11 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
           if (DEQ && ++s2 == S2) {
             s2 = 0;
             ph2 ^= 1;
+          }
+          if (MULTI && g.lazy_dep && i == w.nst - 1) {
+            griddep_wait();
+            unit_chunks(g, w);
+            if (DEQ) nmma += w.nx;
           }
         }
         if (!ok) break;
@@ -1325,9 +1341,13 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
         if (!more) break;
       }
       if (!live) break;
-      const Unit w = unit_of<MULTI>(g, u);  // recomputed: not kept live across the epilogue
-      const int nload = w.nst + w.nx;
+      Unit w = unit_of<MULTI>(g, u);  // recomputed: not kept live across the epilogue
+      const int nload = w.nst + w.nx;  // (a CTA that waits late has one unit)
       if (!MULTI && w.ext && set == 0) write_ext(w);
+      if (MULTI && !DEQ && g.lazy_dep) {
+        griddep_wait();
+        unit_chunks(g, w);
+      }
       if (MULTI && !DEQ && set == 0 && !dead) write_ext_multi(w, k);
       if (DEQ && !dead) {
         for (; cur.i < w.nst; cur.next(NSET, S1, S2)) {
@@ -1338,6 +1358,10 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
         }
         // the adapter position, when it falls to this set
         if (!MULTI && !dead && cur.i == w.nst && w.ext && !pass_ext(cur)) dead = true;
+        if (MULTI && g.lazy_dep) {  // (also after a give-up: the epilogue's counters are the previous grid's)
+          griddep_wait();
+          unit_chunks(g, w);
+        }
         if (MULTI && !dead) {
           for (; cur.i < w.nst + w.nx; cur.next(NSET, S1, S2)) {
             if (!ext_step(w, cur, k)) {
