@@ -1612,6 +1612,9 @@ qnf4_status check_multi_args(int64_t N, int64_t K, int64_t M, int n, int r, bool
   if (n < 1 || n > kMultiMaxAdapters)
     return fail(QNF4_ERR_ARG, "the number of adapters must be in [1, %d] (got %d)", kMultiMaxAdapters, n);
   if (M > 65535 * 128) return fail(QNF4_ERR_SHAPE, "at most %d tokens (got %lld)", 65535 * 128, (long long)M);
+  // rows of the tiles' operand blocks are 32-bit copy coordinates
+  if ((M + 255) / 256 * std::min<int64_t>({n, 256, std::max<int64_t>(M, 1)}) * 256 > INT32_MAX)
+    return fail(QNF4_ERR_SHAPE, "too many tokens for %d adapters (got %lld)", n, (long long)M);
   return QNF4_OK;
 }
 

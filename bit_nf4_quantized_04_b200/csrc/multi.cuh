@@ -27,21 +27,22 @@ constexpr int kMultiThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr int kMultiMaxStages = 8;
 
 // Wait for a phase regardless of the abort flag, within the drain's limit.
-QNF4_DEV void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long wait_ns, unsigned int site) {
+QNF4_DEV bool drain_wait(uint64_t* bar, uint32_t parity, unsigned long long wait_ns, unsigned int site) {
   const long long t0 = wait_clock();
   while (!mbar_try_wait_long(bar, parity)) {
     if (wait_clock() - t0 > ns_cycles(drain_ns(wait_ns))) {
       set_err(site);
-      return;
+      return false;
     }
   }
+  return true;
 }
-// The last copy issued into each of the ring's slots has landed.
+// The last copy issued into each of the ring's slots has landed (within one drain's limit).
 QNF4_DEV void drain_ring(uint64_t* full, int issued, int nst, unsigned long long wait_ns, unsigned int site) {
   const int slots = issued < nst ? issued : nst;
   for (int s = 0; s < slots; ++s) {
     const int j = s + nst * ((issued - 1 - s) / nst);
-    drain_wait(&full[s], static_cast<uint32_t>(j / nst) & 1u, wait_ns, site);
+    if (!drain_wait(&full[s], static_cast<uint32_t>(j / nst) & 1u, wait_ns, site)) return;
   }
 }
 
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   uint8_t* fring = base + kProjRing - static_cast<uint32_t>(nst) * fstage;
   int it = 0;  // steps of earlier batches
   RingPos pos;               // this warp's place in the rings
+  int issued = 0;            // steps whose copies warp 0 has issued
   uint32_t turn_n = 0;       // accumulator turns so far
 
   for (int first = z * g.sb; first < total; first += g.nz * g.sb) {  // alike in the whole cluster
@@ -253,8 +255,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     }
     __syncthreads();
     if (warp == 0) {
-      if (!s_abort) {
-        int issued = it;
+      if (!__shfl_sync(0xffffffffu, s_abort, 0)) {
         bool all = true;
         for (int i = it; i < it + steps && all; ++i, pos.next(nst)) {
           const int s = pos.s;
@@ -276,10 +277,6 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
           if (lane < nb)
             tma_load_2d(fring + static_cast<uint32_t>(s) * fstage + lane * fslot, &g.tmF[job], &full[s], c, s_ad[lane] * g.r);
           ++issued;
-        }
-        if (!all && lane == 0) {
-          for (int i = issued; i < ahead; ++i) mbar_arrive(&full[i]);  // X alone completes these
-          drain_ring(full, issued < ahead ? ahead : issued, nst, g.wait_ns, 92);
         }
       }
       __syncwarp();
@@ -314,10 +311,6 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
           __syncwarp();
           b += last;
         }
-        if (!ok && lane == 0) {
-          mma_commit(&fin_bar);
-          drain_wait(&fin_bar, 0, g.wait_ns, 95);
-        }
       }
       __syncwarp();
     } else {
@@ -329,7 +322,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 #pragma unroll
       for (int c = 0; c < 64; ++c) sum[c] = 0.f;
       const int turns = (steps + kFlushSteps - 1) / kFlushSteps;
-      bool ok = !s_abort;
+      bool ok = !__shfl_sync(0xffffffffu, s_abort, 0);
       for (int t = 0; t < turns && ok; ++t) {
         const uint32_t b = turn_n + t;
         ok = __all_sync(0xffffffffu, wait_or_abort(&acc_full[b & 1], (b / 2) & 1u, g.wait_ns, &s_abort, 94));
@@ -442,9 +435,15 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
     if (g.slices > 1) cluster_wait();
     __syncthreads();
   }
-  if (total <= z * g.sb && warp == 0 && lane == 0) {  // no batch: the first steps of X still land
-    for (int i = 0; i < ahead; ++i) mbar_arrive(&full[i]);
-    drain_ring(full, ahead, nst, g.wait_ns, 92);
+  // Every copy and MMA of this CTA completes before it leaves (they have, unless it gave up or
+  // had no batch: steps of X fetched ahead whose adapter rows were not are completed here).
+  if (warp == 0 && lane == 0) {
+    for (int i = issued; i < ahead; ++i) mbar_arrive(&full[i]);
+    drain_ring(full, issued < ahead ? ahead : issued, nst, g.wait_ns, 92);
+  }
+  if (warp == 1 && lane == 0) {
+    mma_commit(&fin_bar);
+    drain_wait(&fin_bar, 0, g.wait_ns, 95);
   }
   if (total == 0 && ttotal > 0 && z == 0 && rank == 0 && g.exp[job]) {
     // none of these tokens has an adapter, but others of their tile do
@@ -778,7 +777,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
         ++issued;
       }
     }
-    if (!all && lane == 0) drain_ring(full, issued, nst, g.wait_ns, 97);
+    if (lane == 0) drain_ring(full, issued, nst, g.wait_ns, 97);
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16(128, static_cast<uint32_t>(r16), 1u, 0u);
@@ -818,7 +817,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
         b += last;
       }
     }
-    if (!ok && lane == 0) {
+    if (lane == 0) {
       mma_commit(&fin_bar);
       drain_wait(&fin_bar, 0, g.wait_ns, 100);
     }

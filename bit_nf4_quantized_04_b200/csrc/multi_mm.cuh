@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
           }
         }
       }
-      // after a give-up: the loads that both CTAs issued land on the leading CTA's barriers
-      if (!ok && rank == 0) drain_ring(full, it, kMmStages, g.wait_ns, 102);
+      // the copies that both CTAs issued land on the leading CTA's barriers
+      if (rank == 0) drain_ring(full, it, kMmStages, g.wait_ns, 102);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
         }
         if (lane == 0) mma2_commit(&acc_full[k & 1]);
       }
-      if (!ok && lane == 0) {
+      if (lane == 0) {
         mma2_commit(&fin_bar);
         drain_wait(&fin_bar, 0, g.wait_ns, 105);
       }
@@ -433,6 +433,13 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
     tc_fence_before();
   }
   __syncthreads();
+  if (s_abort) {
+    // the other CTA's copies report to the leading one, so after a give-up nobody can wait for
+    // each of them: they have all landed long before this is over (1 ms)
+    const long long t0 = wait_clock();
+    while (wait_clock() - t0 < ns_cycles(1000000)) {
+    }
+  }
   cluster_sync();  // no CTA leaves while the other may still signal it
   if (warp == 1) {
     tc_fence_after();

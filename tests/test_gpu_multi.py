@@ -29,6 +29,9 @@ CASES = [  # N, K, M, n, r, ids
     (384, 640, 64, 64, 64, "tokens"), (264, 960, 130, 5, 33, "runs"), (136, 1024, 300, 8, 8, "wild"),
     (320, 512, 700, 7, 48, "runs"), (1024, 2048, 513, 300, 1, "tokens"), (2048, 1024, 2048, 6, 16, "runs"),
     (128, 64, 256, 2, 64, "none"), (4096, 4096, 1025, 3, 32, "runs"),
+    # the product over a 16-bit base: ranks of each padded width, many adapters per tile, none, one
+    (264, 448, 800, 9, 33, "tokens"), (512, 192, 900, 40, 8, "tokens"), (1000, 320, 769, 2, 64, "one"),
+    (256, 64, 1024, 4, 17, "none"), (136, 576, 1500, 12, 3, "wild"),
 ]
 
 
@@ -115,7 +118,7 @@ def test_backward(case, kind):
     _check_bwd(q, kind, *case, 320)
 
 
-@pytest.mark.parametrize("M", [3, 16, 40, 300])
+@pytest.mark.parametrize("M", [3, 16, 40, 300, 900])
 def test_tokens_of_one_adapter_get_what_the_single_adapter_call_gives(M):
     import bit_nf4_quantized_04_b200 as q
     N, K, n, r = 512, 1024, 4, 16
@@ -133,7 +136,7 @@ def test_tokens_of_one_adapter_get_what_the_single_adapter_call_gives(M):
             assert _norm_off(dX[at], d1[at].double()) <= 2 * BF
 
 
-@pytest.mark.parametrize("M", [1, 16, 40, 300, 600])
+@pytest.mark.parametrize("M", [1, 16, 40, 300, 600, 900])
 @pytest.mark.parametrize("kind", ["nf4", "dense"])
 def test_a_broken_adapter_reaches_its_own_tokens_only(M, kind):
     # adapter 1 holds NaN, +inf and -inf in single rows: its tokens get them there, by IEEE
@@ -172,7 +175,7 @@ def test_a_broken_adapter_reaches_its_own_tokens_only(M, kind):
     q.check()
 
 
-@pytest.mark.parametrize("M", [16, 300])
+@pytest.mark.parametrize("M", [16, 300, 900])
 def test_a_broken_token_stays_alone(M):
     # infinities and NaNs in one token's x and dY: other tokens, and adapters without that
     # token, keep their values
@@ -212,7 +215,7 @@ def test_gradient_of_b_against_differences():
     assert abs(diff) > 3 * bound or (dB * d.double()).abs().sum().item() > 3 * bound
 
 
-@pytest.mark.parametrize("M", [4, 300])
+@pytest.mark.parametrize("M", [4, 300, 900])
 def test_same_bits_every_time_and_in_graphs(M):
     # two captured graphs that share one workspace, replayed in turn on one stream, on the
     # inputs' new values: each equals the eager call
