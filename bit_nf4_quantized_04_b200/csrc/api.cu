@@ -1506,6 +1506,7 @@ qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int
                       size_t ws_bytes, cudaStream_t s) {
   const MultiPlan P = plan_multi(src.kind, src.N, src.K, M, ad.n, ad.r, false, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
+  if (!al16(ws)) return fail(QNF4_ERR_ALIGN, "the workspace must be 16-byte aligned");
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   const ProjJob job{x, ad.A, src.K, reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr};
   qnf4_status st = P.mm ? multi_stage(src, P, ad, false, w8, s) : QNF4_OK;
@@ -1565,6 +1566,7 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   const int main_src = src.kind == A_NF4_K ? A_NF4_MN : A_DENSE_MN;
   const MultiPlan P = plan_multi(main_src, N, K, M, ad.n, ad.r, true, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
+  if (!al16(ws)) return fail(QNF4_ERR_ALIGN, "the workspace must be 16-byte aligned");
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   uint16_t* bt = reinterpret_cast<uint16_t*>(w8 + P.off_bt);
   uint16_t* ptv = reinterpret_cast<uint16_t*>(w8 + P.off_pt);

@@ -15,6 +15,9 @@ GPUs) for the exchanges the path really has.
   double-quantization mean needs the float64 sum of all the matrix's constants, one exact
   all-reduce of a scalar, after which each shard encodes its own constants
   (sharded_quantize_weight), bit-identical to one process.
+* The adapters' gradients of a whole model, summed over the ranks and clipped per adapter
+  (allreduce_clip_adapter_grads): after the sums every rank holds the same gradients, so the
+  norms need no exchange of their own.
 * max_over_ranks: the timing rule of the benchmark (the slowest rank's time).
 
 Every rank must call these functions in the same order with the same arguments' shapes.
@@ -170,6 +173,26 @@ def allreduce_adapter_grads(dA: torch.Tensor, dB: torch.Tensor, group=None) -> N
         return
     tdist.all_reduce(dA, op=tdist.ReduceOp.SUM, group=group)
     tdist.all_reduce(dB, op=tdist.ReduceOp.SUM, group=group)
+
+
+def allreduce_clip_adapter_grads(grads: Sequence[torch.Tensor], max_norm: float, n: int = 1, group=None,
+                                 clip_fn: Callable | None = None) -> torch.Tensor:
+    """In place: the gradients (fp32 or bf16 tensors, each n equal contiguous parts, one per
+    adapter: dA [n, r, K], dB [n, N, r]) summed over the ranks, then every adapter's part scaled
+    by min(1, max_norm / (norm + 1e-6)) of its own norm over the whole list. Returns the norms,
+    fp32 [n], identical on all ranks. `clip_fn(grads, max_norm, n)` clips in place and returns the
+    norms; by default the library's GPU kernels (qnf4_clip_grad_norm)."""
+    grads = list(grads)
+    world, _ = _world(group)
+    if world > 1:
+        for work in [tdist.all_reduce(g, op=tdist.ReduceOp.SUM, group=group, async_op=True) for g in grads]:
+            work.wait()
+    if clip_fn is None:
+        from . import clip_grad_norm
+
+        def clip_fn(gs, m, k):
+            return clip_grad_norm(gs, m, n=k, out=gs)[1]
+    return clip_fn(grads, max_norm, n)
 
 
 def max_over_ranks(x: float, device: torch.device | None = None, group=None) -> float:

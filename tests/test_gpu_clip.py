@@ -183,3 +183,12 @@ def test_refusals_of_the_binding():
             q.clip_grad_norm([g], bad)
     with pytest.raises(ValueError):
         q.grad_norm([g], ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_dist_path_clips_in_place():
+    import bit_nf4_quantized_04_b200 as q
+    from bit_nf4_quantized_04_b200 import dist
+    grads = _grads([(8, 512), (512, 8)], [F, H], 0.02, 12, 3)
+    want, norm = q.clip_grad_norm([t.clone() for t in grads], 0.4, n=3)
+    got = dist.allreduce_clip_adapter_grads(grads, 0.4, 3)
+    assert torch.equal(got, norm) and all(torch.equal(a, b) for a, b in zip(grads, want))

@@ -93,6 +93,7 @@ def test_multi_refusals(q):
         for arg in ("x", "ids", "A", "B", "s"):
             assert f(**{arg: None}) == 1 and f(**{arg: FAKE + 8}) == 3
         assert f(size=16) == 6 and f(ws=None) == 6
+    assert fwd(M=100, ws=FAKE + 8) == 3 and bwd(ws=FAKE + 8) == 3
     assert fwd(M=0, ws=None, size=0) == 0
     assert fwd(h=None) == 1
     assert bwd(w=q.Qnf4Weight(12, 64, 64, 256, FAKE, FAKE, FAKE, FAKE)) == 2   # N not a multiple of 8
