@@ -838,8 +838,8 @@ def run_ours(args):
 
 def run_case(args):
     """One operation on one gate-shaped layer (11008x4096 NF4 weight), or a grouped call
-    over the 7-layer set (quant_group, decode_group), warmup + steps calls and nothing
-    else: the small, L2-exceeding case for ncu captures."""
+    over the 7-layer set (quant_group, decode_group), or many adapters (multi_fwd, multi_bwd,
+    multi_decode, clip), warmup + steps calls and nothing else: the small, L2-exceeding case for ncu captures."""
     import synth
     import bit_nf4_quantized_04_b200 as q
     dev = torch.device("cuda", 0)
@@ -864,6 +864,37 @@ def run_case(args):
         t = time_loop(fn, args.steps, torch.cuda.current_stream())
         q.check()
         print(json.dumps({"case": args.case, "layers": len(shapes), "M": m,
+                          "calls": args.warmup + args.steps, "us_per_call": round(t * 1e6, 2)}))
+        return
+    if args.case in ("multi_fwd", "multi_bwd", "multi_decode", "clip"):
+        # 8 adapters over one gate-shaped base (tokens in runs; 16 tokens of their own adapters for
+        # decoding), or the 14 adapter gradients of the layer set
+        n, shapes = 8, layer_shapes()
+        if args.case == "clip":
+            grads = [synth.normal_bf16((n, *sh), 0.01, synth.SEED_A + i, device=dev).float()
+                     for i, (N, K) in enumerate(shapes) for sh in ((RANK, K), (N, RANK))]
+            out = [torch.empty_like(t) for t in grads]
+            fn = lambda: q.clip_grad_norm(grads, 0.3, n=n, out=out)  # noqa: E731
+            N = K = m = 0
+        else:
+            N, K = 11008, 4096
+            m = 16 if args.case == "multi_decode" else M_TOK
+            w = q.quantize_weight(synth.llama_weight((N, K), synth.SEED_W + 4, device=dev))
+            x = synth.normal_bf16((m, K), 1.0, synth.SEED_X, device=dev)
+            A = synth.normal_bf16((n, RANK, K), 0.01, synth.SEED_A, device=dev)
+            B = synth.normal_bf16((n, N, RANK), 0.01, synth.SEED_B, device=dev)
+            ids = (torch.arange(m, device=dev) * n // m).to(torch.int32)
+            sc = torch.full((n,), ALPHA / RANK, device=dev)
+            if args.case == "multi_bwd":
+                dY = synth.normal_bf16((m, N), 1.0, synth.SEED_DY, device=dev)
+                fn = lambda: q.qlora_linear_multi_bwd(w, x, dY, ids, A, B, sc)  # noqa: E731
+            else:
+                fn = lambda: q.qlora_linear_multi_fwd(w, x, ids, A, B, sc)  # noqa: E731
+        for _ in range(args.warmup):
+            fn()
+        t = time_loop(fn, args.steps, torch.cuda.current_stream())
+        q.check()
+        print(json.dumps({"case": args.case, "N": N, "K": K, "M": m, "adapters": n,
                           "calls": args.warmup + args.steps, "us_per_call": round(t * 1e6, 2)}))
         return
     N, K = 11008, 4096
@@ -977,7 +1008,8 @@ def main():
     ap.add_argument("--no-stack", action="store_true", help="skip the 13B-stack row")
     ap.add_argument("--no-protocol", action="store_true", help="skip the 2 s x 3 session arms")
     ap.add_argument("--case", choices=["fwd", "bwd", "decode", "quant", "chanq_quant", "chanq_fwd", "chanq_bwd",
-                                       "quant_group", "decode_group"], default=None,
+                                       "quant_group", "decode_group", "multi_fwd", "multi_bwd", "multi_decode",
+                                       "clip"], default=None,
                     help="run one operation on one gate-shaped layer (for ncu captures)")
     args = ap.parse_args()
     if args.gpus > 1 and "WORLD_SIZE" not in os.environ:

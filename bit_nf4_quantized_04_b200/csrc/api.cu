@@ -1154,7 +1154,7 @@ constexpr int64_t kMmMinTokens = 768;
 bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
   return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K);
 }
-int stage_grid() { return num_sms() * 4; }
+int stage_grid() { return num_sms() * 6; }
 
 // At most two CTAs per SM, all at once (a CTA costs about 6 us beside its steps, so a second wave
 // of shorter ones loses): first by slices of the contraction (at least two steps each), then,

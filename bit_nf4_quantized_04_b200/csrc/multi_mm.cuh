@@ -82,8 +82,9 @@ QNF4_DEV void mbar_arrive_cluster(uint32_t bar) {
 // ---------------------------------------------------------------------------
 // W_hat as bf16 (each weight bf16(fp32(level * constant)), as the linear layers define it; no
 // work for a 16-bit base), and the adapters' B [n, N, r] or A [n, r, K] copied with rows of rp
-// (zeros past r) and non-finite entries replaced by zero; bad[CTA] says whether it met any. Bound by writing W:
-// 8 codes and one 16-byte store per thread and step.
+// (zeros past r) and non-finite entries replaced by zero; bad[CTA] says whether it met any. Bound by writing W;
+// each packed byte is one lookup of two levels, two products and one conversion. Six CTAs per SM
+// of at most 40 registers (11008 x 4096: 23 us; one code at a time from a level table 30 us).
 struct StageArgs {
   const uint32_t* packed;  // null for a 16-bit base
   const uint8_t* code2;
@@ -99,11 +100,19 @@ struct StageArgs {
   float levels[16];
 };
 
-__global__ void __launch_bounds__(256) k_multi_stage(const __grid_constant__ StageArgs g) {
-  __shared__ float s_lv[16 * 32];  // a copy per lane: no bank conflicts
-  const int tid = threadIdx.x;
+constexpr int kStageCopies = 8;  // of the pair table, one per lane mod 8
+
+__global__ void __launch_bounds__(256, 6) k_multi_stage(const __grid_constant__ StageArgs g) {
+  // entry b, copy j at b * 8 + j: the two levels a packed byte selects. A lane's copy fixes three
+  // bits of the bank pair, so that two lanes of a half warp meet half the time and no more do.
+  __shared__ float2 s_pair[256 * kStageCopies];
+  const int tid = threadIdx.x, lane = tid & 31;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 256 + tid, step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int i = tid; i < 512; i += 256) s_lv[i] = g.levels[i >> 5];
+  if (g.packed)
+    for (int i = tid; i < 256 * kStageCopies; i += 256) {
+      const int b = i / kStageCopies;
+      s_pair[i] = make_float2(g.levels[b >> 4], g.levels[b & 15]);
+    }
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
@@ -144,17 +153,28 @@ __global__ void __launch_bounds__(256) k_multi_stage(const __grid_constant__ Sta
   if (tid == 0) g.bad[blockIdx.x] = any;
   if (!g.packed) return;
   const float mu = *g.mean;
-  const float* lv = s_lv + (tid & 31);
-#pragma unroll 4
-  for (int64_t i = t0; i < g.n8; i += step) {
-    const int64_t b = i >> 3;
-    const float c = fmaf(e4m3_to_f32(__ldg(g.code2 + b)), __ldg(g.scale2 + (b >> 8)), mu);
-    const uint32_t w = __ldg(g.packed + i);
-    uint32_t o[4];
+  const float2* tab = s_pair + (lane & (kStageCopies - 1));
+  const int64_t n1 = g.n8 >> 3;  // blocks
+  // a warp takes 128 words (8 codes each): 16 blocks, whose constants lanes 0-15 make
+  const int64_t wstep = static_cast<int64_t>(gridDim.x) * 8 * 128;
+#pragma unroll 2
+  for (int64_t w0 = (static_cast<int64_t>(blockIdx.x) * 8 + (tid >> 5)) * 128; w0 < g.n8; w0 += wstep) {
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_bf16x2(lv[((w >> (8 * j + 4)) & 15u) * 32] * c, lv[((w >> (8 * j)) & 15u) * 32] * c);
-    reinterpret_cast<uint4*>(g.W)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < 4; ++k) w[k] = w0 + 32 * k + lane < g.n8 ? __ldg(g.packed + w0 + 32 * k + lane) : 0u;
+    const int64_t b = (w0 >> 3) + (lane & 15);
+    const float mine = b < n1 ? fmaf(e4m3_to_f32(__ldg(g.code2 + b)), __ldg(g.scale2 + (b >> 8)), mu) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float c = __shfl_sync(0xffffffffu, mine, 4 * k + (lane >> 3));
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = tab[__byte_perm(w[k], 0u, 0x4440u + j) * kStageCopies];
+        o[j] = pack_bf16x2(v.x * c, v.y * c);
+      }
+      if (w0 + 32 * k + lane < g.n8) reinterpret_cast<uint4*>(g.W)[w0 + 32 * k + lane] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
