@@ -530,8 +530,20 @@ def _multi_ws(need: int, like: torch.Tensor, ws):
     return ws, ws.numel() * ws.element_size()
 
 
-def _multi_fwd(fn: str, base, N, K, x, ids, A, B, scales, h, ws):
+def _multi_base(x: torch.Tensor, *base: torch.Tensor) -> None:
+    d = x.get_device()
+    for t in base:
+        if t.get_device() != d:
+            raise ValueError("the base weight must be on the tensors' device")
+
+
+def _nf4_tensors(w: Nf4Weight):
+    return w.packed, w.code2, w.scale2, w.mean
+
+
+def _multi_fwd(fn: str, base, bts, N, K, x, ids, A, B, scales, h, ws):
     M, n, r = _multi_args(N, K, x, ids, A, B, scales)
+    _multi_base(x, *bts)
     h = x.new_empty((M, N)) if h is None else _multi_out(h, (M, N), torch.bfloat16, "h", x)
     if M == 0:
         return h
@@ -542,8 +554,9 @@ def _multi_fwd(fn: str, base, N, K, x, ids, A, B, scales, h, ws):
     return h
 
 
-def _multi_bwd(fn: str, base, N, K, x, dY, ids, A, B, scales, dX, dA, dB, ws):
+def _multi_bwd(fn: str, base, bts, N, K, x, dY, ids, A, B, scales, dX, dA, dB, ws):
     M, n, r = _multi_args(N, K, x, ids, A, B, scales, dY)
+    _multi_base(x, *bts)
     dX = _multi_out(dX, (M, K), torch.bfloat16, "dX", x)
     dA = _multi_out(dA, (n, r, K), torch.float32, "dA", x)
     dB = _multi_out(dB, (n, N, r), torch.float32, "dB", x)
@@ -566,26 +579,27 @@ def qlora_linear_multi_fwd(w: Nf4Weight, x: torch.Tensor, ids: torch.Tensor, A: 
     ids int32 [M], in any order; an id outside 0 .. n - 1 (e.g. -1) means no adapter. A
     [n, r, K], B [n, N, r] bf16 (pad an adapter of a lower rank with zero rows of A), scales
     fp32 [n]."""
-    return _multi_fwd("qnf4_qlora_linear_multi_fwd", (C.byref(w.c()),), w.N, w.K, x, ids, A, B, scales, h, ws)
+    return _multi_fwd("qnf4_qlora_linear_multi_fwd", (C.byref(w.c()),), _nf4_tensors(w), w.N, w.K, x, ids, A, B,
+                      scales, h, ws)
 
 
 def dense_linear_multi_fwd(W: torch.Tensor, x, ids, A, B, scales, h=None, ws=None) -> torch.Tensor:
     """``qlora_linear_multi_fwd`` over a 16-bit (protected) base W bf16 [N, K]."""
     N, K = _req(W, torch.bfloat16, "W").shape
-    return _multi_fwd("qnf4_dense_linear_multi_fwd", (W.data_ptr(), N, K), N, K, x, ids, A, B, scales, h, ws)
+    return _multi_fwd("qnf4_dense_linear_multi_fwd", (W.data_ptr(), N, K), (W,), N, K, x, ids, A, B, scales, h, ws)
 
 
 def qlora_linear_multi_bwd(w: Nf4Weight, x, dY, ids, A, B, scales, dX=None, dA=None, dB=None, ws=None):
     """Backward of ``qlora_linear_multi_fwd``: (dX bf16 [M, K], dA fp32 [n, r, K], dB fp32
     [n, N, r]), dA[a] and dB[a] summed over the tokens of adapter a (zeros without any)."""
-    return _multi_bwd("qnf4_qlora_linear_multi_bwd", (C.byref(w.c()),), w.N, w.K, x, dY, ids, A, B, scales,
-                      dX, dA, dB, ws)
+    return _multi_bwd("qnf4_qlora_linear_multi_bwd", (C.byref(w.c()),), _nf4_tensors(w), w.N, w.K, x, dY, ids, A,
+                      B, scales, dX, dA, dB, ws)
 
 
 def dense_linear_multi_bwd(W: torch.Tensor, x, dY, ids, A, B, scales, dX=None, dA=None, dB=None, ws=None):
     """``qlora_linear_multi_bwd`` over a 16-bit (protected) base W bf16 [N, K]."""
     N, K = _req(W, torch.bfloat16, "W").shape
-    return _multi_bwd("qnf4_dense_linear_multi_bwd", (W.data_ptr(), N, K), N, K, x, dY, ids, A, B, scales,
+    return _multi_bwd("qnf4_dense_linear_multi_bwd", (W.data_ptr(), N, K), (W,), N, K, x, dY, ids, A, B, scales,
                       dX, dA, dB, ws)
 
 
@@ -602,6 +616,7 @@ def qlora_linear_multi_fwd_group(ws_: list, xs: list, ids: torch.Tensor, As: lis
     for w, x, A, B in zip(ws_[1:], xs[1:], As[1:], Bs[1:]):
         if _multi_args(w.N, w.K, x, ids, A, B, scales) != (M, n, r):
             raise ValueError("every layer takes the same tokens, adapters and rank")
+    _multi_base(xs[0], *[t for w in ws_ for t in _nf4_tensors(w)])
     if hs is None:
         hs = [xs[0].new_empty((M, w.N)) for w in ws_]
     else:
@@ -658,6 +673,9 @@ def _grad_call(grads, n: int, norm, ws, max_norm=None, out=None):
         live = [p for p, m in zip(optr, num) if m]
         if len(set(live)) != len(live):
             raise ValueError("an output appears twice")
+        ins = set(ptr)
+        if not same and any(o != p and o in ins for o, p, m in zip(optr, ptr, num) if m):
+            raise ValueError("an output is another gradient's buffer")
         args += (float(max_norm), optr.buffer_info()[0])
     with _on(like):
         wsb, size = _multi_ws(max(int(lib.qnf4_grad_workspace_size(len(grads), a[2], n)), 16), like, ws)

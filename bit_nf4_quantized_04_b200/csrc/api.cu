@@ -1152,7 +1152,8 @@ struct MultiPlan {
 // 512 tokens, 54 / 53 at 1024; bf16 41 / 44, 50 / 45; backward NF4 68 / 72, 86 / 75)
 constexpr int64_t kMmMinTokens = 768;
 bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
-  return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K);
+  return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K) &&
+         n * N <= INT32_MAX;  // rows of the copies are 32-bit coordinates
 }
 int stage_grid() { return num_sms() * 6; }
 

@@ -192,3 +192,15 @@ def test_dist_path_clips_in_place():
     want, norm = q.clip_grad_norm([t.clone() for t in grads], 0.4, n=3)
     got = dist.allreduce_clip_adapter_grads(grads, 0.4, 3)
     assert torch.equal(got, norm) and all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+def test_an_output_that_is_another_gradient_is_refused():
+    """Scaling into each other's buffers would read what another part has already written."""
+    import bit_nf4_quantized_04_b200 as q
+    a, b = torch.ones(4, 6, device="cuda"), torch.ones(4, 6, device="cuda")
+    with pytest.raises(ValueError, match="another gradient"):
+        q.clip_grad_norm([a, b], 1.0, out=[b, a])
+    with pytest.raises(ValueError, match="another gradient"):
+        q.clip_grad_norm([a, b], 1.0, out=[torch.empty_like(a), a])
+    out, _ = q.clip_grad_norm([a, b], 1.0, out=[a.view(4, 6), torch.empty_like(b)])  # its own buffer, as a view
+    assert out[0].data_ptr() == a.data_ptr() and torch.equal(a, out[1])

@@ -354,3 +354,45 @@ def test_long_contractions_and_partial_tiles(case, kind):
     base, _, fwd, bwd = _base(q, kind, synth.llama_weight((N, K), 620, device="cuda"))
     one, two = [[fwd(base, x, ids, A, B, s), *bwd(base, x, dY, ids, A, B, s)] for _ in range(2)]
     assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+@pytest.mark.parametrize("M", [7, 130, 900])
+def test_the_most_adapters(M):
+    """The limit on adapters (4096), the last of them named, with few tokens for each."""
+    import bit_nf4_quantized_04_b200 as q
+    N, K, n, r = 64, 128, 4096, 2
+    x, A, B, dY, ids, s = _inputs(N, K, M, n, r, "tokens", 551)
+    ids[M // 2] = n - 1
+    w = q.quantize_weight(torch.zeros(N, K, dtype=torch.bfloat16, device="cuda"))
+    for base, fwd, bwd in ((w, q.qlora_linear_multi_fwd, q.qlora_linear_multi_bwd),
+                           (q.dequant(w).bfloat16(), q.dense_linear_multi_fwd, q.dense_linear_multi_bwd)):
+        h = fwd(base, x, ids, A, B, s)
+        dX, dA, dB = bwd(base, x, dY, ids, A, B, s)
+        q.check()
+        want, mag, _ = multi_ref.forward(q.dequant(w), x, ids, A, B, s)
+        _within(h, want, BF * want.abs() * 1.01 + BF * 1.01 * mag + U2 * (K / 16 + 64) * mag * 2, "h")
+        (wX, mX, _), (wA, pA, cA), (wB, pB, cB) = multi_ref.backward(q.dequant(w), x, dY, ids, A, B, s)
+        _within(dX, wX, BF * wX.abs() * 1.01 + BF * 1.01 * mX + U2 * (N / 16 + 64) * mX * 2, "dX")
+        tok = BF ** 3 + U2 * (M / 16 + 64)
+        _within(dA, wA, tok * pA + U2 * (N / 16 + 64) * cA, "dA")
+        _within(dB, wB, tok * pB + U2 * (K / 16 + 64) * cB, "dB")
+    with pytest.raises(q.Qnf4Error, match="ERR_ARG"):
+        q.qlora_linear_multi_fwd(w, x, ids, torch.cat([A, A[:1]]), torch.cat([B, B[:1]]), torch.cat([s, s[:1]]))
+
+
+def test_a_base_on_another_device_is_refused():
+    import bit_nf4_quantized_04_b200 as q
+    N, K, M, n, r = 128, 64, 5, 3, 4
+    x, A, B, dY, ids, s = _inputs(N, K, M, n, r, "tokens", 552)
+    W = synth.llama_weight((N, K), 552, device="cuda")
+    w = q.quantize_weight(W)
+    far = q.Nf4Weight(N, K, w.packed, w.code2.cpu(), w.scale2, w.mean)
+    with pytest.raises(ValueError, match="base weight"):
+        q.qlora_linear_multi_fwd(far, x, ids, A, B, s)
+    with pytest.raises(ValueError, match="base weight"):
+        q.qlora_linear_multi_fwd_group([w, far], [x, x], ids, [A, A], [B, B], s)
+    with pytest.raises(ValueError, match="base weight"):
+        q.qlora_linear_multi_bwd(far, x, dY, ids, A, B, s)
+    for f, args in ((q.dense_linear_multi_fwd, (x,)), (q.dense_linear_multi_bwd, (x, dY))):
+        with pytest.raises(ValueError):
+            f(W.cpu(), *args, ids, A, B, s)
