@@ -519,6 +519,22 @@ def _multi_out(t, shape, dtype, name: str, like):
     return t
 
 
+def _apart(given, others) -> None:
+    """A buffer that the caller gave for an output must overlap none of the others: the kernels of a
+    call run into one another, so it would be written while it is still read."""
+    def span(t):
+        p = t.data_ptr()
+        return p, p + t.numel() * t.element_size()
+
+    taken = [span(t) for t in others if t is not None]
+    for t in given:
+        if t is not None:
+            t0, t1 = span(t)
+            if any([t0 < o1 and o0 < t1 for o0, o1 in taken]):
+                raise ValueError("an output overlaps another argument")
+            taken.append((t0, t1))
+
+
 def _multi_ws(need: int, like: torch.Tensor, ws):
     """(pointer owner, its bytes) of the caller's workspace, or of a new one."""
     if ws is None:  # (elements of the tensor's own type: one keyword less to parse per call)
@@ -530,11 +546,9 @@ def _multi_ws(need: int, like: torch.Tensor, ws):
     return ws, ws.numel() * ws.element_size()
 
 
-def _multi_base(x: torch.Tensor, *base: torch.Tensor) -> None:
-    d = x.get_device()
-    for t in base:
-        if t.get_device() != d:
-            raise ValueError("the base weight must be on the tensors' device")
+def _multi_base(x: torch.Tensor, base) -> None:
+    if set(map(_get_device, base)) != {x.get_device()}:
+        raise ValueError("the base weight must be on the tensors' device")
 
 
 def _nf4_tensors(w: Nf4Weight):
@@ -543,7 +557,9 @@ def _nf4_tensors(w: Nf4Weight):
 
 def _multi_fwd(fn: str, base, bts, N, K, x, ids, A, B, scales, h, ws):
     M, n, r = _multi_args(N, K, x, ids, A, B, scales)
-    _multi_base(x, *bts)
+    _multi_base(x, bts)
+    if h is not None:
+        _apart((h,), (x, A, B, ids, scales, ws, *bts))
     h = x.new_empty((M, N)) if h is None else _multi_out(h, (M, N), torch.bfloat16, "h", x)
     if M == 0:
         return h
@@ -556,7 +572,9 @@ def _multi_fwd(fn: str, base, bts, N, K, x, ids, A, B, scales, h, ws):
 
 def _multi_bwd(fn: str, base, bts, N, K, x, dY, ids, A, B, scales, dX, dA, dB, ws):
     M, n, r = _multi_args(N, K, x, ids, A, B, scales, dY)
-    _multi_base(x, *bts)
+    _multi_base(x, bts)
+    if dX is not None or dA is not None or dB is not None:
+        _apart((dX, dA, dB), (x, dY, A, B, ids, scales, ws, *bts))
     dX = _multi_out(dX, (M, K), torch.bfloat16, "dX", x)
     dA = _multi_out(dA, (n, r, K), torch.float32, "dA", x)
     dB = _multi_out(dB, (n, N, r), torch.float32, "dB", x)
@@ -616,10 +634,11 @@ def qlora_linear_multi_fwd_group(ws_: list, xs: list, ids: torch.Tensor, As: lis
     for w, x, A, B in zip(ws_[1:], xs[1:], As[1:], Bs[1:]):
         if _multi_args(w.N, w.K, x, ids, A, B, scales) != (M, n, r):
             raise ValueError("every layer takes the same tokens, adapters and rank")
-    _multi_base(xs[0], *[t for w in ws_ for t in _nf4_tensors(w)])
+    _multi_base(xs[0], [t for w in ws_ for t in _nf4_tensors(w)])
     if hs is None:
         hs = [xs[0].new_empty((M, w.N)) for w in ws_]
     else:
+        _apart(hs, (*xs, ids, scales, ws))
         hs = [_multi_out(h, (M, w.N), torch.bfloat16, "h", xs[0]) for w, h in zip(ws_, hs, strict=True)]
     ptrs = lambda ts: (C.c_void_p * k)(*[t.data_ptr() for t in ts])  # noqa: E731
     with _on(xs[0]):
@@ -639,8 +658,8 @@ _data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
 
 
 def _grad_list(ts, what: str):
-    """Host arrays (pointers, dtypes, element counts) of a list of gradients, and its device.
-    One C-level pass per property: the list of a whole model is a thousand tensors."""
+    """Pointers, dtypes and element counts of a list of gradients, and its device. One C-level pass
+    per property: the list of a whole model is a thousand tensors."""
     dts = list(map(_dtype_of, ts))
     for dt in set(dts):
         if dt not in _GRAD_DTYPES:
@@ -650,33 +669,35 @@ def _grad_list(ts, what: str):
         raise ValueError(f"{what} must be CUDA tensors on one device")
     if not all(map(_is_contiguous, ts)):
         raise ValueError(f"{what} must be contiguous")
-    return (array("Q", list(map(_data_ptr, ts))), array("i", list(map(_GRAD_DTYPES.__getitem__, dts))),
-            array("q", list(map(_numel, ts))), devs.pop())
+    return list(map(_data_ptr, ts)), dts, list(map(_numel, ts)), devs.pop()
 
 
 def _grad_call(grads, n: int, norm, ws, max_norm=None, out=None):
     if not grads:
         raise ValueError("the list of gradients is empty")
-    ptr, dt, num, dev = _grad_list(grads, "gradients")
+    ptr, dts, num, dev = _grad_list(grads, "gradients")
     like = grads[0]
     if norm is None:
         norm = like.new_empty(n, dtype=torch.float32)
     elif _req(norm, torch.float32, "norm").numel() != n or norm.get_device() != dev:
         raise ValueError(f"norm must hold {n} values on the gradients' device")
-    a = [v.buffer_info()[0] for v in (ptr, dt, num)]
+    arrays = [array("Q", ptr), array("i", list(map(_GRAD_DTYPES.__getitem__, dts))), array("q", num)]
+    a = [v.buffer_info()[0] for v in arrays]
     args = (len(grads), *a, n)
     if out is not None:
         same = len(out) == len(grads) and all(map(_IS, out, grads))
-        optr, odt, onum, odev = (ptr, dt, num, dev) if same else _grad_list(out, "outputs")
-        if odt != dt or onum != num or odev != dev:
+        optr, odts, onum, odev = (ptr, dts, num, dev) if same else _grad_list(out, "outputs")
+        if odts != dts or onum != num or odev != dev:
             raise ValueError("one output per gradient, of its dtype, size and device")
-        live = [p for p, m in zip(optr, num) if m]
-        if len(set(live)) != len(live):
-            raise ValueError("an output appears twice")
-        ins = set(ptr)
-        if not same and any(o != p and o in ins for o, p, m in zip(optr, ptr, num) if m):
-            raise ValueError("an output is another gradient's buffer")
-        args += (float(max_norm), optr.buffer_info()[0])
+        if len(set(optr)) != len(optr):  # (empty tensors share the null pointer)
+            live = [p for p, m in zip(optr, num) if m]
+            if len(set(live)) != len(live):
+                raise ValueError("an output appears twice")
+        if not same and not (ins := set(ptr)).isdisjoint(optr):
+            if any(o != p and o in ins for o, p, m in zip(optr, ptr, num) if m):
+                raise ValueError("an output is another gradient's buffer")
+        arrays.append(array("Q", optr))
+        args += (float(max_norm), arrays[3].buffer_info()[0])
     with _on(like):
         wsb, size = _multi_ws(max(int(lib.qnf4_grad_workspace_size(len(grads), a[2], n)), 16), like, ws)
         _lib.call("qnf4_grad_norm" if out is None else "qnf4_clip_grad_norm", *args, norm.data_ptr(),

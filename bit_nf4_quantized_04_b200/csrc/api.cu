@@ -1162,13 +1162,19 @@ int stage_grid() { return num_sms() * 6; }
 // where few tokens name many adapters, by taking the batches of slots in parallel and making
 // them smaller. With 1024 tokens and more the token tiles fill the SMs, and a tile rarely
 // names more adapters than one batch holds, so its CTAs take the batches one after another.
-ProjPlan plan_proj(int64_t M, int64_t csteps, int jobs, int dmax, int per, int r16, int nsm) {
+// The backward's two projections (csteps, the longer, and csteps2) share a launch, the longer one's
+// CTAs first; where those alone would outlast an even share of all the steps by a quarter, both are
+// cut further and a second wave of shorter CTAs fills up (5120 x 13824, 8192 tokens: 86 us, 117 uncut).
+ProjPlan plan_proj(int64_t M, int64_t csteps, int64_t csteps2, int dmax, int per, int r16, int nsm) {
   ProjPlan p;
-  const int64_t tiles = (M + 127) / 128 * jobs;
+  const int64_t tiles = (M + 127) / 128 * (csteps2 ? 2 : 1);
   const int slots = (dmax + per - 1) / per * per;
   const int sbmax = kProjMaxCols / r16 / per * per;
   p.sb = std::min(slots, sbmax);
   while (p.slices < 8 && tiles * 2 * p.slices <= 2 * nsm && csteps / (2 * p.slices) >= 2) p.slices *= 2;
+  while (csteps2 && p.slices < 8 && csteps / (2 * p.slices) >= 16 &&
+         csteps / p.slices * 2 * nsm > (M + 127) / 128 * (csteps + csteps2) * 5 / 4)
+    p.slices *= 2;
   auto batches = [&] { return (slots + p.sb - 1) / p.sb; };
   while (p.sb > per && tiles * p.slices * batches() < nsm) p.sb = std::max(per, p.sb / 2 / per * per);
   p.nz = static_cast<int>(std::min<int64_t>(batches(), std::max<int64_t>(1, 2 * nsm / (tiles * p.slices))));
@@ -1202,7 +1208,7 @@ MultiPlan plan_multi(int main_src, int64_t N, int64_t K, int64_t M, int n, int r
   const int width = P.mm ? P.rp : 64;
   P.dmax = static_cast<int>(std::min<int64_t>({n, P.tn, M}));
   P.cmax = (P.dmax + P.per - 1) / P.per;
-  P.proj = plan_proj(M, (bwd ? std::max(N, K) : K) / 64, bwd ? 2 : 1, P.dmax, P.per, P.r16, nsm);
+  P.proj = plan_proj(M, (bwd ? std::max(N, K) : K) / 64, bwd ? std::max<int64_t>(1, std::min(N, K) / 64) : 0, P.dmax, P.per, P.r16, nsm);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1297,7 +1303,7 @@ struct ProjJob {
 };
 
 qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const ProjJob* jobs, int njobs,
-                       int lazy, uint8_t* w8, cudaStream_t s) {
+                       uint8_t* w8, cudaStream_t s) {
   static thread_local ProjArgs g;
   std::memset(&g, 0, sizeof(g));
   const int xrows = static_cast<int>(std::min<int64_t>(128, (M + 15) / 16 * 16));
@@ -1311,6 +1317,7 @@ qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const 
     g.exp[i] = j.exp;
     g.pt[i] = j.pt;
   }
+  g.swap = njobs > 1 && jobs[1].C > jobs[0].C;
   g.ids = ad.ids;
   g.scales = ad.scales;
   g.pos = reinterpret_cast<const int*>(w8 + P.off_pos);
@@ -1332,7 +1339,6 @@ qnf4_status multi_proj(const MultiPlan& P, const Adapters& ad, int64_t M, const 
   g.ctr = reinterpret_cast<unsigned*>(w8 + P.off_ctr);
   g.nctr = P.mm ? 0 : static_cast<int>(P.main.tiles());
   g.width = P.mm ? P.rp : 64;
-  g.lazy = lazy;
   g.wait_ns = g_wait_ns;
   launch_multi_kernel(k_multi_proj, g_proj_smem_set,
                       dim3(P.proj.slices, static_cast<unsigned>((M + 127) / 128), njobs * P.proj.nz), kMultiThreads,
@@ -1496,6 +1502,7 @@ qnf4_status multi_mm(const BaseSrc& src, const MultiPlan& P, const Adapters& ad,
   g.js = MN ? K : ad.r;
   g.r = ad.r;
   g.n = ad.n;
+  g.wait_ext = MN ? 0 : 1;
   g.wait_ns = g_wait_ns;
   if (g_ev_start) cudaEventRecord(g_ev_start, s);
   launch_multi_kernel(k_multi_mm<MN>, g_mm_smem_set[MN], dim3(2 * std::min(pairs, g.tt * g.ft)), kMultiThreads, kMmSmem, 2, s, g);
@@ -1511,7 +1518,8 @@ qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   const ProjJob job{x, ad.A, src.K, reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr};
   qnf4_status st = P.mm ? multi_stage(src, P, ad, false, w8, s) : QNF4_OK;
-  if (st == QNF4_OK) st = multi_proj(P, ad, M, &job, 1, P.mm, w8, s);
+  // (k_multi_mm relies on the projections' wait for the grid before them, see there)
+  if (st == QNF4_OK) st = multi_proj(P, ad, M, &job, 1, w8, s);
   if (st != QNF4_OK) return st;
   if (P.mm) return multi_mm<false>(src, P, ad, x, M, h, w8, s);
   return multi_main(src, src.kind, P, ad, x, M, ad.B, ad.r, src.N * ad.r, h, w8, s);
@@ -1600,7 +1608,7 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   st = launched("multi_prep");
   if (st != QNF4_OK) return st;
   const ProjJob jobs[2] = {{dY, bt, N, reinterpret_cast<uint16_t*>(w8 + P.off_exp), ptv}, {x, ad.A, K, nullptr, ptu}};
-  st = multi_proj(P, ad, M, jobs, 2, 0, w8, s);
+  st = multi_proj(P, ad, M, jobs, 2, w8, s);
   if (st != QNF4_OK) return st;
   st = multi_grad(P, ad, x, dY, M, N, K, ptv, ptu, dA, dB, w8, s);
   if (st != QNF4_OK) return st;

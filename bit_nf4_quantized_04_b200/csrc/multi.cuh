@@ -97,6 +97,7 @@ static_assert(128u * 68u * 4u + 128u * 64u * 4u <= kProjRing, "the sums reuse th
 struct ProjArgs {
   CUtensorMap tmX[2], tmF[2];  // X [M, C] in boxes of xrows x 64, F [n r, C] in boxes of r16 x 64
   int nsteps[2];
+  int swap;                    // the second job is the longer one: its CTAs come first
   uint16_t* exp[2];            // operand blocks [tiles][cmax][tn][width], or null
   uint16_t* pt[2];             // parts [3 r16][ldp], or null
   const int* ids;
@@ -105,7 +106,6 @@ struct ProjArgs {
   int64_t M, ldp;
   int n, r, r16, per, tn, dmax, cmax;
   int width;                   // columns of an operand block: 64, or the padded rank (per = 1)
-  int lazy;                    // the previous grid's results are not read here: wait for it at the end
   int sb, nz;                  // slots per batch; CTA z takes the batches z, z + nz, ...
   int slices;                  // cluster size
   int xrows;                   // rows of X fetched per step: 128, or fewer tokens rounded up to 16
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   uint8_t* base = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = g.slices > 1 ? cluster_rank() : 0u;  // == blockIdx.x
-  const int job = blockIdx.z / g.nz, z = blockIdx.z - job * g.nz;
+  const int jz = blockIdx.z / g.nz, job = jz ^ g.swap, z = blockIdx.z - jz * g.nz;
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int64_t tile = row0 / g.tn;
   const int words = (g.n + 31) >> 5;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  if (!g.lazy) griddep_wait();
+  griddep_wait();
   griddep_launch_dependents();
 
   const int r16 = g.r16;
@@ -455,7 +455,6 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
             make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  if (g.lazy) griddep_wait();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -496,7 +495,7 @@ struct PrepArgs {
   int64_t N;
   uint4* clear;      // 16-byte words to clear
   int64_t nclear;
-  int lazy;          // as in ProjArgs
+  int lazy;          // the previous grid's results are not read here: wait for it at the end
 };
 
 constexpr int kPrepThreads = 1024;

@@ -213,6 +213,7 @@ struct MmArgs {
   const uint16_t* exp;
   int64_t as, js;
   int r, n;
+  int wait_ext;         // E, cnt and list come from the previous grid
   unsigned long long wait_ns;
 };
 
@@ -224,14 +225,14 @@ __device__ __noinline__ float mm_fix(const MmArgs& g, int64_t t, int64_t f) {
   if (static_cast<unsigned>(a) >= static_cast<unsigned>(g.n)) return 0.f;
   const int64_t tile = t >> 8;
   int slot = 0;
-  while (slot < g.cnt[tile] && g.list[tile * g.dmax + slot] != a) ++slot;
+  while (slot < __ldcg(g.cnt + tile) && __ldcg(g.list + tile * g.dmax + slot) != a) ++slot;
   const uint16_t* u = g.exp + ((tile * g.dmax + slot) * 256 + (t & 255)) * g.rp;
   const uint16_t* e = g.ext + a * g.as;
   float s = 0.f;
   for (int j = 0; j < g.r; ++j) {
     const uint16_t b = MN ? e[j * g.js + f] : e[f * g.js + j];
     if ((b & 0x7F80u) == 0x7F80u)
-      s += __uint_as_float(static_cast<uint32_t>(b) << 16) * __uint_as_float(static_cast<uint32_t>(u[j]) << 16);
+      s += __uint_as_float(static_cast<uint32_t>(b) << 16) * __uint_as_float(static_cast<uint32_t>(__ldcg(u + j)) << 16);
   }
   return s;
 }
@@ -285,7 +286,12 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
   cluster_sync();  // the pair's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  griddep_wait();
+  // Not waited for here: the previous grid. It is the projections' (forward) or the gradients' (dX),
+  // which let this one in only after their own wait, so whatever ran before them has completed: the
+  // 16-bit base and the adapters' copies, and for dX the projections too. A pair so starts when its
+  // two SMs are free, under the previous grid's last CTAs, and only the forward's adapter positions
+  // wait for that grid. What earlier grids wrote is read from L2 (TMA, ld.cg). (5120 x 5120, 1531
+  // tokens: 91 us instead of 95; backward of 4096 x 4096, 4096 tokens: 146 instead of 156.)
   griddep_launch_dependents();
 
   const int tiles = g.tt * g.ft;
@@ -305,38 +311,47 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
         int t, f;
         tile_of(u, t, f);
         const int32_t tok = t * 256 + static_cast<int>(rank) * 128, feat = f * 256 + static_cast<int>(rank) * 128;
-        const int nx = g.cnt[t];
-        for (int i = 0; i < g.nk + nx; ++i, ++it) {
-          const int s = it % kMmStages;
-          ok = it < kMmStages || wait_or_abort(&empty[s], static_cast<uint32_t>(it / kMmStages - 1) & 1u, g.wait_ns, &s_abort, 101, true);
+        auto slot = [&]() -> bool {
+          return it < kMmStages || wait_or_abort(&empty[it % kMmStages], static_cast<uint32_t>(it / kMmStages - 1) & 1u,
+                                                 g.wait_ns, &s_abort, 101, true);
+        };
+        for (int i = 0; i < g.nk; ++i, ++it) {
+          ok = slot();
           if (!ok) break;
+          const int s = it % kMmStages;
           uint8_t* st = base + s * kMmStage;
           const uint32_t bar = map_to_cta(&full[s], 0);
-          if (i < g.nk) {
-            if (rank == 0) mbar_expect_tx(&full[s], 2u * kMmStage);
+          if (rank == 0) mbar_expect_tx(&full[s], 2u * kMmStage);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint8_t* sh = st + h * kMmHalf;
-              const int32_t c = i * 128 + h * 64;
-              tma_load_2d_pair(sh, &g.tmX, bar, c, tok);
-              if (!MN) {
-                tma_load_2d_pair(sh + 16384, &g.tmW, bar, c, feat);
-              } else {
-                tma_load_2d_pair(sh + 16384, &g.tmW, bar, feat, c);
-                tma_load_2d_pair(sh + 24576, &g.tmW, bar, feat + 64, c);
-              }
-            }
-          } else {
-            const int x = i - g.nk, a = g.list[static_cast<int64_t>(t) * g.dmax + x];
-            const uint32_t bytes = 256u * static_cast<uint32_t>(g.rp);  // of either operand
-            if (rank == 0) mbar_expect_tx(&full[s], 4u * bytes);
-            tma_load_2d_pair(st, &g.tmE, bar, 0, (t * g.dmax + x) * 256 + static_cast<int>(rank) * 128);
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* sh = st + h * kMmHalf;
+            const int32_t c = i * 128 + h * 64;
+            tma_load_2d_pair(sh, &g.tmX, bar, c, tok);
             if (!MN) {
-              tma_load_2d_pair(st + 16384, &g.tmG, bar, 0, static_cast<int32_t>(a * g.grows + feat));
+              tma_load_2d_pair(sh + 16384, &g.tmW, bar, c, feat);
             } else {
-              tma_load_2d_pair(st + 16384, &g.tmG, bar, feat, static_cast<int32_t>(a * g.grows));
-              tma_load_2d_pair(st + 16384 + bytes / 2, &g.tmG, bar, feat + 64, static_cast<int32_t>(a * g.grows));
+              tma_load_2d_pair(sh + 16384, &g.tmW, bar, feat, c);
+              tma_load_2d_pair(sh + 24576, &g.tmW, bar, feat + 64, c);
             }
+          }
+        }
+        if (!ok) break;
+        if (g.wait_ext) griddep_wait();
+        const int nx = __ldcg(g.cnt + t);
+        for (int x = 0; x < nx; ++x, ++it) {
+          ok = slot();
+          if (!ok) break;
+          const int s = it % kMmStages, a = __ldcg(g.list + static_cast<int64_t>(t) * g.dmax + x);
+          uint8_t* st = base + s * kMmStage;
+          const uint32_t bar = map_to_cta(&full[s], 0);
+          const uint32_t bytes = 256u * static_cast<uint32_t>(g.rp);  // of either operand
+          if (rank == 0) mbar_expect_tx(&full[s], 4u * bytes);
+          tma_load_2d_pair(st, &g.tmE, bar, 0, (t * g.dmax + x) * 256 + static_cast<int>(rank) * 128);
+          if (!MN) {
+            tma_load_2d_pair(st + 16384, &g.tmG, bar, 0, static_cast<int32_t>(a * g.grows + feat));
+          } else {
+            tma_load_2d_pair(st + 16384, &g.tmG, bar, feat, static_cast<int32_t>(a * g.grows));
+            tma_load_2d_pair(st + 16384 + bytes / 2, &g.tmG, bar, feat + 64, static_cast<int32_t>(a * g.grows));
           }
         }
       }
@@ -360,34 +375,42 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
       for (int u = pair; u < tiles && ok; u += npair, ++k) {
         int t, f;
         tile_of(u, t, f);
-        const int nx = g.cnt[t];
         if (k >= 2) ok = wait_or_abort(&acc_free[k & 1], static_cast<uint32_t>(k / 2 - 1) & 1u, g.wait_ns, &s_abort, 103);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(k & 1) * 256u;
-        for (int i = 0; i < g.nk + nx; ++i, p.next(kMmStages)) {
-          const int s = p.s;
-          ok = __all_sync(0xffffffffu, wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 104));
+        for (int i = 0; i < g.nk; ++i, p.next(kMmStages)) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(&full[p.s], p.ph, g.wait_ns, &s_abort, 104));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t so = static_cast<uint32_t>(s) * (kMmStage >> 4);
-          if (i < g.nk) {
-            const uint64_t ad = ad0 + so, bd = bd0 + so;
-            if (lane == 0) {
+          const uint32_t so = static_cast<uint32_t>(p.s) * (kMmStage >> 4);
+          const uint64_t ad = ad0 + so, bd = bd0 + so;
+          if (lane == 0) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t h = (kk >> 2) * (kMmHalf >> 4), k4 = kk & 3;
-                mma2_ss(d, ad + h + 2u * k4, bd + h + (MN ? (2048u >> 4) : 2u) * k4, idesc, (i > 0 || kk > 0) ? 1u : 0u);
-              }
-              mma2_commit(&empty[s]);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t h = (kk >> 2) * (kMmHalf >> 4), k4 = kk & 3;
+              mma2_ss(d, ad + h + 2u * k4, bd + h + (MN ? (2048u >> 4) : 2u) * k4, idesc, (i > 0 || kk > 0) ? 1u : 0u);
             }
-          } else if (lane == 0) {
-            const uint64_t ad = ae0 + so, bd = be0 + so;
-            for (int kk = 0; kk < g.rp / 16; ++kk) mma2_ss(d, ad + 2u * kk, bd + (MN ? (2048u >> 4) : 2u) * kk, idesc, 1u);
-            mma2_commit(&empty[s]);
+            mma2_commit(&empty[p.s]);
           }
           __syncwarp();
+        }
+        if (ok) {
+          if (g.wait_ext) griddep_wait();
+          const int nx = __ldcg(g.cnt + t);
+          for (int x = 0; x < nx; ++x, p.next(kMmStages)) {
+            ok = __all_sync(0xffffffffu, wait_or_abort(&full[p.s], p.ph, g.wait_ns, &s_abort, 104));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t so = static_cast<uint32_t>(p.s) * (kMmStage >> 4);
+            const uint64_t ad = ae0 + so, bd = be0 + so;
+            if (lane == 0) {
+              for (int kk = 0; kk < g.rp / 16; ++kk) mma2_ss(d, ad + 2u * kk, bd + (MN ? (2048u >> 4) : 2u) * kk, idesc, 1u);
+              mma2_commit(&empty[p.s]);
+            }
+            __syncwarp();
+          }
         }
         if (lane == 0) mma2_commit(&acc_full[k & 1]);
       }
@@ -401,7 +424,7 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
     const int q = warp & 3;
     uint8_t* out = base + kMmStages * kMmStage + q * 8192;
     int met = 0;
-    for (int i = lane; i < g.nbad; i += 32) met |= g.bad[i];
+    for (int i = lane; i < g.nbad; i += 32) met |= __ldcg(g.bad + i);
     const bool bad = __any_sync(0xffffffffu, met != 0);
     int k = 0, piece = 0;
     for (int u = pair; u < tiles; u += npair, ++k) {
@@ -423,6 +446,7 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
         }
         const int64_t f0 = static_cast<int64_t>(f) * 256 + c * 64;
         if (bad) {
+          if (g.wait_ext) griddep_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             v0[j] = __float_as_uint(__uint_as_float(v0[j]) + mm_fix<MN>(g, tok0 + lane, f0 + j));
@@ -452,6 +476,7 @@ __global__ void __launch_bounds__(kMultiThreads, 1) k_multi_mm(const __grid_cons
     __syncwarp();
     tc_fence_before();
   }
+  griddep_wait();  // so that this grid's end is also the end of all before it
   __syncthreads();
   if (s_abort) {
     // the other CTA's copies report to the leading one, so after a give-up nobody can wait for

@@ -396,3 +396,23 @@ def test_a_base_on_another_device_is_refused():
     for f, args in ((q.dense_linear_multi_fwd, (x,)), (q.dense_linear_multi_bwd, (x, dY))):
         with pytest.raises(ValueError):
             f(W.cpu(), *args, ids, A, B, s)
+
+
+def test_outputs_that_overlap_an_argument_are_refused():
+    import bit_nf4_quantized_04_b200 as q
+    N = K = 128
+    M, n, r = 64, 3, 4
+    x, A, B, dY, ids, s = _inputs(N, K, M, n, r, "tokens", 553)
+    w = q.quantize_weight(synth.llama_weight((N, K), 553, device="cuda"))
+    dA = torch.empty(n, r, K, device="cuda")
+    room = torch.empty(M + 1, N, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        q.qlora_linear_multi_fwd(w, x, ids, A, B, s, h=x)
+    for kw in (dict(dX=x), dict(dX=dY), dict(dA=dA, dB=dA.view(n, N, r))):
+        with pytest.raises(ValueError, match="overlaps"):
+            q.qlora_linear_multi_bwd(w, x, dY, ids, A, B, s, **kw)
+    with pytest.raises(ValueError, match="overlaps"):
+        q.qlora_linear_multi_fwd_group([w, w], [x[:8], x[:8]], ids[:8], [A, A], [B, B], s, hs=[room[:8], room[4:12]])
+    # neighbours are no overlap
+    h = q.qlora_linear_multi_fwd(w, x, ids, A, B, s, h=room[1:])
+    assert torch.equal(h, q.qlora_linear_multi_fwd(w, x, ids, A, B, s))
