@@ -689,13 +689,6 @@ def _grad_call(grads, n: int, norm, ws, max_norm=None, out=None):
         optr, odts, onum, odev = (ptr, dts, num, dev) if same else _grad_list(out, "outputs")
         if odts != dts or onum != num or odev != dev:
             raise ValueError("one output per gradient, of its dtype, size and device")
-        if len(set(optr)) != len(optr):  # (empty tensors share the null pointer)
-            live = [p for p, m in zip(optr, num) if m]
-            if len(set(live)) != len(live):
-                raise ValueError("an output appears twice")
-        if not same and not (ins := set(ptr)).isdisjoint(optr):
-            if any(o != p and o in ins for o, p, m in zip(optr, ptr, num) if m):
-                raise ValueError("an output is another gradient's buffer")
         arrays.append(array("Q", optr))
         args += (float(max_norm), arrays[3].buffer_info()[0])
     with _on(like):

@@ -1652,6 +1652,36 @@ size_t grad_ws_bytes(int32_t count, const int64_t* elems, int32_t n) {
          align256(static_cast<size_t>(n) * sizeof(float));
 }
 
+// An output is its own gradient's buffer or overlaps no gradient, and no two outputs overlap: else
+// one piece would read what another has already written.
+qnf4_status check_grad_outputs(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                               void* const* out) {
+  struct Span {
+    uintptr_t at, end;
+    int32_t t;
+  };
+  auto span = [&](const void* p, int32_t t) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return Span{at, at + static_cast<uintptr_t>(elems[t]) * (dtype[t] == QNF4_OUT_BF16 ? 2 : 4), t};
+  };
+  std::vector<Span> v;
+  v.reserve(static_cast<size_t>(count));
+  for (int32_t t = 0; t < count; ++t)
+    if (elems[t]) v.push_back(span(out[t], t));
+  const auto before = [](const Span& a, const Span& b) { return a.at < b.at; };
+  if (!std::is_sorted(v.begin(), v.end(), before)) std::sort(v.begin(), v.end(), before);
+  for (size_t i = 1; i < v.size(); ++i)
+    if (v[i].at < v[i - 1].end) return fail(QNF4_ERR_ARG, "outputs %d and %d overlap", v[i - 1].t, v[i].t);
+  for (int32_t t = 0; t < count; ++t) {
+    if (!elems[t] || out[t] == g[t]) continue;
+    const Span in = span(g[t], t);
+    auto it = std::lower_bound(v.begin(), v.end(), in, before);  // the outputs are disjoint: ends ascend too
+    if ((it != v.end() && it->at < in.end) || (it != v.begin() && (it - 1)->end > in.at))
+      return fail(QNF4_ERR_ARG, "an output overlaps gradient %d", t);
+  }
+  return QNF4_OK;
+}
+
 qnf4_status check_grad_args(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
                             int32_t n, void* const* out, const float* norm) {
   if (count < 0) return fail(QNF4_ERR_ARG, "count must be >= 0 (got %d)", count);
@@ -1670,7 +1700,7 @@ qnf4_status check_grad_args(int32_t count, const void* const* g, const int32_t* 
     if (reinterpret_cast<uintptr_t>(g[t]) % es || (out && reinterpret_cast<uintptr_t>(out[t]) % es))
       return fail(QNF4_ERR_ALIGN, "tensor %d: not aligned to its element size", t);
   }
-  return QNF4_OK;
+  return out ? check_grad_outputs(count, g, dtype, elems, out) : QNF4_OK;
 }
 
 // The launches' table of tensors [t0, t0 + count).

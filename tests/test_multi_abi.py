@@ -126,3 +126,17 @@ def test_multi_group_refusals(q):
     assert f(x=None) == 1 and f(ids=None) == 1 and f(s=FAKE + 4) == 3 and f(ids=FAKE + 4) == 3
     assert f(n=0) == 1 and f(r=65) == 1 and f(r=0) == 1
     assert f(A=(C.c_void_p * 2)(FAKE, None)) == 1
+
+
+def test_clip_outputs_that_overlap(q):
+    f = q.lib.qnf4_clip_grad_norm
+    keep, a = _grad_args(ptrs=(FAKE, FAKE + 4096), elems=(12, 24))   # 48 bytes, 48 bytes
+
+    def st(o0, o1):
+        out = (C.c_void_p * 2)(o0, o1)
+        return f(2, *a, 1, 1.0, C.addressof(out), FAKE, FAKE, 16, None)  # (the workspace is too small)
+
+    assert st(FAKE, FAKE + 4096) == 6 and st(FAKE + 48, FAKE + 96) == 6 and st(FAKE + 8192, FAKE + 4096) == 6
+    assert st(FAKE + 8192, FAKE + 8192) == 1 and st(FAKE + 8192, FAKE + 8192 + 46) == 1   # one another
+    assert st(FAKE + 4096, FAKE + 8192) == 1 and st(FAKE + 4100, FAKE + 8192) == 1        # another gradient
+    assert st(FAKE + 4, FAKE + 8192) == 1 and st(FAKE + 8192, FAKE + 46) == 1             # part of a gradient
