@@ -65,12 +65,18 @@ struct RingPos {
 // Projections onto the tokens' own adapters
 // ---------------------------------------------------------------------------
 // P[m][0 .. r) = scales[a] sum_c X[m, c] F[a][0 .. r)[c]. A CTA takes 128 tokens, a batch of the
-// adapters that they name (its slots) and a slice of the contraction; X and the adapters' rows come by TMA (128-byte swizzle), one MMA of N = slots x
-// r16 multiplies every token with every slot, and the epilogue keeps each token's own slot:
-// with a few slots per tile the extra products cost nothing beside the stream of X, and rows
-// of different tokens or adapters never mix. The slices of a contraction are the CTAs of a
-// cluster: each leaves its tokens' sums in shared memory and adds up a share of the tokens
-// over all of them, in rank order.
+// adapters that they name (its slots) and a slice of the contraction; X and the adapters' rows come
+// by TMA (128-byte swizzle), one MMA of N = slots x r16 multiplies every token with every slot, and
+// the epilogue keeps each token's own slot: with a few slots per tile the extra products cost nothing
+// beside the stream of X, and rows of different tokens or adapters never mix. The slices of a
+// contraction are the CTAs of a cluster: each leaves its tokens' sums in shared memory and adds up a
+// share of the tokens over all of them, in rank order.
+//
+// Bound by reading X, and with few tokens by what a CTA spends beside its steps: 2 us to find the
+// adapters, 1 us of cluster barrier, 1 us to add up, 2 us to store. Measured: 4096 tokens of 8
+// adapters of r = 16, C = 4096, 18 us (1.9 TB/s, X from HBM); both projections of 8192 tokens of
+// r = 64, C = 5120 and 13824, 86 us (3.6 TB/s). A ring twice as long at one CTA per SM was slower
+// (2048 tokens, C = 4096: the whole forward 71 us instead of 65).
 //
 // The tensor cores' additions truncate: a bf16 sum of C products in one accumulator comes out
 // short by 1.1e-9 C relative (measured: 9.1e-6 at C = 8192), which fp32 gradients would show.
@@ -465,13 +471,16 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 // ---------------------------------------------------------------------------
 // Backward preparation
 // ---------------------------------------------------------------------------
-// CTA 0 sorts the tokens by adapter (stable, so equal calls sum in equal order; every warp
-// takes a run of tokens and, where the table of all warps' positions fits, walks it without a
-// barrier, else the warps take 32 tokens each in turn): adapter a's tokens take the positions off[a] .. off[a] + count, each adapter starting on a multiple of
-// 64, with the adapter's last token repeated up to its end (their projections are zero).
+// CTA 0 sorts the tokens by adapter (stable, so equal calls sum in equal order; every warp takes a
+// run of tokens and, where the table of all warps' positions fits, walks it without a barrier, else
+// the warps take 32 tokens each in turn): adapter a's tokens take the positions off[a] .. off[a] +
+// count, each adapter starting on a multiple of 64, with the adapter's last token repeated up to its
+// end (their projections are zero).
 // It cuts every adapter's 64-token steps into slices of at most `lsteps` (one empty slice for
 // an adapter without tokens), the work list of k_multi_grad. The other CTAs transpose B
-// [n, N, r] into BT [n, r, N], clear the projections' parts and the counters.
+// [n, N, r] into BT [n, r, N], clear the projections' parts and the counters. Bound by the latency
+// of CTA 0's passes over the ids: 6 us for 4096 tokens of 4 adapters, 10 us for 8192 of 8 (one CTA
+// keeps the sort free of a grid-wide barrier; by many tokens it runs under the stage kernel's end).
 struct GradSlice {
   int a, p0, steps;
   int count;   // slices of this adapter
@@ -674,16 +683,17 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
 // and P = v for dA, X = dY and P = u for dB, both in one launch. A CTA takes 128 features and
 // the slices blockIdx.y, blockIdx.y + gridDim.y, ... of the adapters' tokens, with the loads of the
 // next slice on their way while one is written out (many adapters of a few tokens each make short
-// slices, and a CTA for each spent its time on setting up); 64 tokens a step: the TMA warp gathers their rows (four
-// rows per instruction, one instruction per lane) into an MN-major tile, or, where they follow one
-// another as the tokens of a request or sample do, copies them in two boxes; the three parts of P
-// come as a K-major tile of 3 r16 rows, and two MMAs multiply X with them: the first two parts
-// into an accumulator each, the third, 2^-8 of the second, on top of the second's. As in the projections two
-// pairs of accumulators take turns of kFlushSteps steps and are added up in registers.
+// slices, and a CTA for each spent its time on setting up); 64 tokens a step: the TMA warp gathers
+// their rows (four rows per instruction, one instruction per lane) into an MN-major tile, or, where
+// they follow one another as the tokens of a request or sample do, copies them in two boxes; the
+// three parts of P come as a K-major tile of 3 r16 rows, and two MMAs multiply X with them: the first
+// two parts into an accumulator each, the third, 2^-8 of the second, on top of the second's. As in
+// the projections two pairs of accumulators take turns of kFlushSteps steps and are added up in registers.
 // The work is bound by reading X once (it is often still in L2 from the projections); tokens
 // of other adapters are never read, so neither their number nor their values matter. An
 // adapter of several slices goes through fp32 partial tiles that the last of its CTAs to
-// finish adds up in slice order.
+// finish adds up in slice order. Measured: 4096 tokens of 8 adapters of r = 16, 4096 and 11008
+// features, 36 us (3.6 TB/s); 8192 tokens of r = 64, 13824 and 5120 features, 79 us (3.9 TB/s).
 struct MultiGradArgs {
   CUtensorMap tmX[2];  // x [M, K], dY [M, N]: boxes of 1 x 64, for gathers
   CUtensorMap tmR[2];  // the same in boxes of 64 x 64
