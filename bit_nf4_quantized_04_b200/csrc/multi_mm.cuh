@@ -24,8 +24,9 @@
 // padded to rp and freed of non-finite entries (whose products the epilogue adds to their own
 // adapter's tokens, only if there are any: mm_fix).
 //
-// Bound by the tensor pipe (89 to 90 % busy over the kernel): 4096 tokens through 11008 x 4096 with 8
-// adapters of r = 16, 225 us forward (1651 TFLOP/s), 241 us for dX (1536). What is left is the last
+// Bound by the tensor pipe (89 to 94 % busy over the kernel): 4096 tokens through 11008 x 4096 with 8
+// adapters of r = 16, 225 to 245 us forward (1651 to 1514 TFLOP/s) and 241 to 258 us for dX (1536 to
+// 1433) on two boxes, whose clocks under this load differ. What is left is the last
 // wave of tiles; cutting it along the contraction with partial tiles through L2 lost (5120 x 5120,
 // 1531 tokens: 113 us for the call instead of 105 at the time), so tiles stay whole.
 #pragma once
