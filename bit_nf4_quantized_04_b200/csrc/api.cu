@@ -686,6 +686,10 @@ qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int
   size_t need = 0;
   for (int l = 0; l < n; ++l) need += decode_ws_bytes(w[l].K, M, r);
   if (!ws || ws_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, need);
+  // (the sums in it are read in fp32 words; many adapters keep the ABI's 16 bytes at every M)
+  const uintptr_t unit = ids ? 16u : sizeof(float);
+  if (reinterpret_cast<uintptr_t>(ws) % unit)
+    return fail(QNF4_ERR_ALIGN, "the workspace must be %zu-byte aligned", static_cast<size_t>(unit));
   static thread_local DecodeArgs a;  // about 10 KB: kept off the stack
   std::memset(&a, 0, sizeof(a));
   a.n = n;
