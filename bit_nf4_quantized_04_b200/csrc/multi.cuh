@@ -61,6 +61,32 @@ struct RingPos {
   }
 };
 
+// v as three bf16 parts that add up to it exactly (24 bits, 8 to a part), all of v's sign and none
+// of them zero unless v is: an infinity they are multiplied with then gives three infinities of one
+// sign, whose sum is what the product with v would be. (Rounding to nearest gives parts of either
+// sign, and zeros where fewer parts are enough.) Infinities and NaNs are their own three parts.
+// (Below 2^-125 the last part may vanish.)
+QNF4_DEV void bf16_parts(float v, uint16_t (&h)[3]) {
+  auto head = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); };  // toward zero
+  if (!isfinite(v)) {
+    h[0] = h[1] = h[2] = f2bf(v);
+    return;
+  }
+  float p0 = head(v), p1 = v - p0, p2;
+  if (p1 == 0.f) {  // 8 bits: halves and quarters
+    p0 = 0.5f * v;
+    p1 = p2 = 0.25f * v;
+  } else {
+    const float rest = p1;
+    p1 = head(rest);
+    p2 = rest - p1;
+    if (p2 == 0.f) p1 = p2 = 0.5f * rest;
+  }
+  const float p[3] = {p0, p1, p2};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) h[k] = static_cast<uint16_t>(__float_as_uint(p[k]) >> 16);
+}
+
 // ---------------------------------------------------------------------------
 // Projections onto the tokens' own adapters
 // ---------------------------------------------------------------------------
@@ -89,7 +115,7 @@ struct RingPos {
 //
 // Outputs: the main product's operand blocks (bf16 s u, zeros in the other slots), the tile's
 // list of adapters, and for the gradients the values in three bf16 parts that add up to the
-// fp32 value (8 bits each), transposed to [3 r16][sorted token].
+// fp32 value (bf16_parts), transposed to [3 r16][sorted token].
 constexpr int kFlushSteps = 4;
 constexpr uint32_t kProjRing = 104u * 1024u;
 constexpr uint32_t kProjSmem = 1024u + kProjRing;  // two CTAs per SM
@@ -423,15 +449,12 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
         const int j = i / share, row = i - j * share;
         const int mine = s_slot[r0 + row] - first;
         if (mine < 0 || mine >= nb) continue;
-        float v = fin[row * r16 + j];
+        uint16_t h[3];
+        bf16_parts(fin[row * r16 + j], h);
         int64_t at = j * g.ldp + g.pos[row0 + r0 + row];
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          const uint16_t h = f2bf(v);
-          g.pt[job][at] = h;
-          // nothing remains of an infinity or a NaN (the difference would be NaN)
-          v = isfinite(v) ? v - __uint_as_float(static_cast<uint32_t>(h) << 16) : 0.f;
-          if (!isfinite(v)) v = 0.f;
+          g.pt[job][at] = h[k];
           at += static_cast<int64_t>(r16) * g.ldp;
         }
       }
