@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 // run of tokens and, where the table of all warps' positions fits, walks it without a barrier, else
 // the warps take 32 tokens each in turn): adapter a's tokens take the positions off[a] .. off[a] +
 // count, each adapter starting on a multiple of 64, with the adapter's last token repeated up to its
-// end (their projections are zero).
+// end (k_multi_grad fetches those rows and clears them).
 // It cuts every adapter's 64-token steps into slices of at most `lsteps` (one empty slice for
 // an adapter without tokens), the work list of k_multi_grad. The other CTAs transpose B
 // [n, N, r] into BT [n, r, N], clear the projections' parts and the counters. Bound by the latency
@@ -510,7 +510,7 @@ struct GradSlice {
   int index;   // this one among them
   int group;   // ordinal among the adapters of more than one slice, for counters
   int part0;   // first of the adapter's slices among those of such adapters, for partials
-  int pad;
+  int tail;    // tokens of the last step, the rest of whose 64 positions is padding
 };
 
 struct PrepArgs {
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_multi_prep(const __grid_consta
           const int st = steps - i * g.lsteps;
           if (in_bounds(ex[1] + i < g.slmax, 92))
             g.slices[ex[1] + i] = GradSlice{a, (ex[0] + i * g.lsteps) * 64, st < g.lsteps ? st : g.lsteps, sl, i,
-                                            ex[2], ex[3], 0};
+                                            ex[2], ex[3], i == sl - 1 && (c & 63) ? c & 63 : 64};
         }
       }
       __syncthreads();
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
     uint32_t b = 0;
     RingPos p;
     for (int y = blockIdx.y; y < nsl && ok; y += gridDim.y) {
-      const int steps = g.slices[y].steps;
+      const int steps = g.slices[y].steps, tail = g.slices[y].tail;
       for (int i = 0; i < steps && ok; ++i, p.next(nst)) {
         const int s = p.s, turn = i % kFlushSteps;
         if (turn == 0 && b >= 2)
@@ -829,6 +829,17 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_grad(const __grid_co
         ok = ok && wait_or_abort(&full[s], p.ph, g.wait_ns, &s_abort, 98);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (i == steps - 1 && tail < 64) {
+          // the rows past the adapter's tokens: their P is zero, but zero times an infinity is NaN
+          // (a row is 128 bytes of either half, whatever the swizzle)
+          uint8_t* rest = base + static_cast<uint32_t>(s) * stage + static_cast<uint32_t>(tail) * 128u;
+          for (int c = lane; c < (64 - tail) * 8; c += 32) {
+            reinterpret_cast<uint4*>(rest)[c] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(rest + 8192)[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
         tc_fence_after();
         const uint32_t so = (static_cast<uint32_t>(s) * stage) >> 4;
         const uint64_t ad = ad0 + so, bd = bd0 + so;

@@ -70,3 +70,14 @@ def test_infinities_with_every_step_full(kind, bad):
     # two adapters of 64 tokens each
     ids = (torch.arange(128, device="cuda") // 64).to(torch.int32)
     _check(kind, ids, *BAD[bad])
+
+
+@pytest.mark.parametrize("kind", ["nf4", "dense"])
+@pytest.mark.parametrize("M", [1, 5, 16, 33, 70, 131, 300, 900])
+def test_infinities_in_the_last_token_of_an_adapter(kind, M):
+    ids = (torch.arange(M, device="cuda") % 3).to(torch.int32)
+    if M > 4:
+        ids[M // 2] = -1
+    _check(kind, ids, [(M - 1, 11, -INF)], [])
+    _check(kind, ids, [], [(M - 1, 13, INF)])
+    _check(kind, ids, [(M - 1, 11, INF)], [(max(M - 2, 0), 13, INF)])
