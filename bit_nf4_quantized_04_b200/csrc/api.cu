@@ -676,6 +676,38 @@ cudaError_t launch_decode(const DecodeArgs& a, int P, cudaStream_t s) {
   return launch_pdl(k_nf4_decode<Q, MULTI>, dim3(P), dim3(kDecBlockThreads), kDecSmem, s, a, g_wait_ns);
 }
 
+// A buffer of a call, and lists of them: a many-adapter call's kernels (and the layers of a group)
+// run into one another, so one that it writes may overlap no other.
+struct Buf {
+  const void* p = nullptr;
+  size_t bytes = 0;
+};
+struct BufList {
+  Buf v[64];
+  int n = 0;
+  void add(const void* p, int64_t elems, size_t size) { v[n++] = Buf{p, static_cast<size_t>(elems) * size}; }
+};
+qnf4_status check_apart(const BufList& written, const BufList& read) {
+  auto meet = [](const Buf& a, const Buf& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.bytes && y < x + a.bytes;
+  };
+  for (int i = 0; i < written.n; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(written.v[i], written.v[j])) return fail(QNF4_ERR_ARG, "an output overlaps another one");
+    for (int j = 0; j < read.n; ++j)
+      if (meet(written.v[i], read.v[j])) return fail(QNF4_ERR_ARG, "an output overlaps another argument");
+  }
+  return QNF4_OK;
+}
+void add_nf4(BufList* b, const qnf4_weight& w) {
+  const int64_t nb = w.N * w.K / 64;
+  b->add(w.packed, nb, 32);
+  b->add(w.code2, nb, 1);
+  b->add(w.scale2, (nb + 255) / 256, sizeof(float));
+  b->add(w.mean, 1, sizeof(float));
+}
+
 // Decode-size forward of n independent layers in one launch pair (k_lora_u, then
 // k_nf4_decode); the layers share M, r and scale, or with ids their many adapters (nad of
 // them, with their scales; As and Bs are then stacks). Arguments are checked by the caller.
@@ -690,6 +722,21 @@ qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int
   const uintptr_t unit = ids ? 16u : sizeof(float);
   if (reinterpret_cast<uintptr_t>(ws) % unit)
     return fail(QNF4_ERR_ALIGN, "the workspace must be %zu-byte aligned", static_cast<size_t>(unit));
+  if (ids) {
+    static_assert(7 * kDecMaxGroup + 2 <= 64, "the lists hold a group");
+    BufList out, in;
+    in.add(ids, M, sizeof(int));
+    in.add(scales, nad, sizeof(float));
+    for (int l = 0; l < n; ++l) {
+      out.add(hs[l], M * w[l].N, 2);
+      in.add(xs[l], M * w[l].K, 2);
+      in.add(As[l], nad * r * w[l].K, 2);
+      in.add(Bs[l], nad * w[l].N * r, 2);
+      add_nf4(&in, w[l]);
+    }
+    const qnf4_status st = check_apart(out, in);
+    if (st != QNF4_OK) return st;
+  }
   static thread_local DecodeArgs a;  // about 10 KB: kept off the stack
   std::memset(&a, 0, sizeof(a));
   a.n = n;
@@ -1514,14 +1561,32 @@ qnf4_status multi_mm(const BaseSrc& src, const MultiPlan& P, const Adapters& ad,
   return launched("multi_mm");
 }
 
+// What a many-adapter call reads, beside its X and dY.
+void add_reads(BufList* b, const BaseSrc& src, const Adapters& ad, int64_t M) {
+  b->add(ad.ids, M, sizeof(int));
+  b->add(ad.scales, ad.n, sizeof(float));
+  b->add(ad.A, ad.n * ad.r * src.K, 2);
+  b->add(ad.B, ad.n * src.N * ad.r, 2);
+  if (src.w)
+    add_nf4(b, *src.w);
+  else
+    b->add(src.Wd, src.N * src.K, 2);
+}
+
 qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int64_t M, void* h, void* ws,
                       size_t ws_bytes, cudaStream_t s) {
   const MultiPlan P = plan_multi(src.kind, src.N, src.K, M, ad.n, ad.r, false, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   if (!al16(ws)) return fail(QNF4_ERR_ALIGN, "the workspace must be 16-byte aligned");
+  BufList out, in;
+  out.add(h, M * src.N, 2);
+  in.add(x, M * src.K, 2);
+  add_reads(&in, src, ad, M);
+  qnf4_status st = check_apart(out, in);
+  if (st != QNF4_OK) return st;
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   const ProjJob job{x, ad.A, src.K, reinterpret_cast<uint16_t*>(w8 + P.off_exp), nullptr};
-  qnf4_status st = P.mm ? multi_stage(src, P, ad, false, w8, s) : QNF4_OK;
+  if (P.mm) st = multi_stage(src, P, ad, false, w8, s);
   // (k_multi_mm relies on the projections' wait for the grid before them, see there)
   if (st == QNF4_OK) st = multi_proj(P, ad, M, &job, 1, w8, s);
   if (st != QNF4_OK) return st;
@@ -1580,6 +1645,15 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   const MultiPlan P = plan_multi(main_src, N, K, M, ad.n, ad.r, true, num_sms());
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   if (!al16(ws)) return fail(QNF4_ERR_ALIGN, "the workspace must be 16-byte aligned");
+  BufList out, in;
+  out.add(dX, M * K, 2);
+  out.add(dA, ad.n * ad.r * K, sizeof(float));
+  out.add(dB, ad.n * N * ad.r, sizeof(float));
+  in.add(x, M * K, 2);
+  in.add(dY, M * N, 2);
+  add_reads(&in, src, ad, M);
+  qnf4_status st = check_apart(out, in);
+  if (st != QNF4_OK) return st;
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   uint16_t* bt = reinterpret_cast<uint16_t*>(w8 + P.off_bt);
   uint16_t* ptv = reinterpret_cast<uint16_t*>(w8 + P.off_pt);
@@ -1604,7 +1678,7 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   pr.clear = reinterpret_cast<uint4*>(w8 + P.off_pt);
   pr.nclear = static_cast<int64_t>(P.off_clear_end - P.off_pt) / 16;
   pr.lazy = P.mm;
-  qnf4_status st = P.mm ? multi_stage(src, P, ad, true, w8, s) : QNF4_OK;
+  if (P.mm) st = multi_stage(src, P, ad, true, w8, s);
   if (st != QNF4_OK) return st;
   const int64_t blocks = std::max<int64_t>(ad.n * ((N + 63) / 64), 8);
   launch_pdl(k_multi_prep, dim3(1 + static_cast<unsigned>(std::min<int64_t>(blocks, num_sms()))), dim3(kPrepThreads),

@@ -6,7 +6,7 @@ import pytest
 
 FAKE = 1 << 20  # never dereferenced
 BIG = 1 << 40
-ERR_ALIGN = 3
+ERR_ARG, ERR_ALIGN = 1, 3
 
 
 @pytest.fixture(scope="module")
@@ -34,3 +34,59 @@ def test_a_workspace_off_its_alignment_is_refused(q, M, off):
             st += [lib.qnf4_qlora_linear_fwd(C.byref(w), FAKE, M, FAKE, FAKE, 8, 1.0, FAKE, ws, BIG, None),
                    lib.qnf4_qlora_linear_fwd_group(2, ws_, p, M, p, p, 8, 1.0, p, ws, BIG, None)]
     assert st == [ERR_ALIGN] * len(st)
+
+
+class Buffers:
+    """Addresses of one many-adapter call's buffers, each of its own megabyte."""
+    N, K, n, r = 64, 128, 3, 8
+
+    def __init__(self, q, M, first=0):
+        self.q, self.M = q, M
+        names = ("packed code2 scale2 mean W x dY ids A B s h dX dA dB ws").split()
+        for i, k in enumerate(names):
+            setattr(self, k, FAKE * (1 + first + i))
+
+    def weight(self):
+        return self.q.Qnf4Weight(self.N, self.K, 64, 256, self.packed, self.code2, self.scale2, self.mean)
+
+    def call(self, fn):
+        b, w = self, self.weight()
+        base = (C.byref(w),) if "qlora" in fn else (b.W, b.N, b.K)
+        d = (b.dY,) if fn.endswith("bwd") else ()
+        out = (b.dX, b.dA, b.dB) if fn.endswith("bwd") else (b.h,)
+        return getattr(self.q.lib, "qnf4_" + fn)(*base, b.x, *d, b.M, b.ids, b.n, b.A, b.B, b.r, b.s, *out, b.ws, BIG, None)
+
+
+READ = {"qlora": "packed code2 scale2 mean x ids A B s", "dense": "W x ids A B s"}
+
+
+@pytest.mark.parametrize("M", [1, 16, 100, 1000])
+@pytest.mark.parametrize("fn", ["qlora_linear_multi_fwd", "dense_linear_multi_fwd", "qlora_linear_multi_bwd",
+                                "dense_linear_multi_bwd"])
+def test_an_output_over_another_buffer_is_refused(q, fn, M):
+    bwd = fn.endswith("bwd")
+    for out in ("dX", "dA", "dB") if bwd else ("h",):
+        for other in READ[fn[:5]].split() + (["dY", "dX", "dA", "dB"] if bwd else []):
+            if other != out:
+                b = Buffers(q, M)
+                setattr(b, out, getattr(b, other))
+                assert b.call(fn) == ERR_ARG, (out, other)
+                b = Buffers(q, M)
+                setattr(b, other, getattr(b, out) + 16 if other != "mean" else getattr(b, out))  # inside the output
+                assert b.call(fn) == ERR_ARG, (out, other)
+
+
+def _group(q, ls, n, r):
+    ws_ = (q.Qnf4Weight * len(ls))(*[b.weight() for b in ls])
+    p = lambda k: (C.c_void_p * len(ls))(*[getattr(b, k) for b in ls])  # noqa: E731
+    return q.lib.qnf4_qlora_linear_multi_fwd_group(len(ls), ws_, p("x"), ls[0].M, ls[0].ids, n, p("A"), p("B"), r,
+                                                   ls[0].s, p("h"), ls[0].ws, BIG, None)
+
+
+@pytest.mark.parametrize("layers", [2, 8])
+def test_a_grouped_output_over_any_layers_buffer_is_refused(q, layers):
+    for other in READ["qlora"].split() + ["h"]:
+        for at in range(1, layers) if other not in ("ids", "s") else (0,):
+            ls = [Buffers(q, 4, 16 * i) for i in range(layers)]
+            ls[0].h = getattr(ls[at], other)
+            assert _group(q, ls, 3, 8) == ERR_ARG, (other, at)
