@@ -694,9 +694,9 @@ qnf4_status check_apart(const BufList& written, const BufList& read) {
   };
   for (int i = 0; i < written.n; ++i) {
     for (int j = 0; j < i; ++j)
-      if (meet(written.v[i], written.v[j])) return fail(QNF4_ERR_ARG, "an output overlaps another one");
+      if (meet(written.v[i], written.v[j])) return fail(QNF4_ERR_ARG, "an output or the workspace overlaps another one");
     for (int j = 0; j < read.n; ++j)
-      if (meet(written.v[i], read.v[j])) return fail(QNF4_ERR_ARG, "an output overlaps another argument");
+      if (meet(written.v[i], read.v[j])) return fail(QNF4_ERR_ARG, "an output or the workspace overlaps another argument");
   }
   return QNF4_OK;
 }
@@ -725,6 +725,7 @@ qnf4_status decode_group(int n, const qnf4_weight* w, const void* const* xs, int
   if (ids) {
     static_assert(7 * kDecMaxGroup + 2 <= 64, "the lists hold a group");
     BufList out, in;
+    out.add(ws, static_cast<int64_t>(need), 1);
     in.add(ids, M, sizeof(int));
     in.add(scales, nad, sizeof(float));
     for (int l = 0; l < n; ++l) {
@@ -1579,6 +1580,7 @@ qnf4_status multi_fwd(const BaseSrc& src, const Adapters& ad, const void* x, int
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   if (!al16(ws)) return fail(QNF4_ERR_ALIGN, "the workspace must be 16-byte aligned");
   BufList out, in;
+  out.add(ws, static_cast<int64_t>(P.total), 1);
   out.add(h, M * src.N, 2);
   in.add(x, M * src.K, 2);
   add_reads(&in, src, ad, M);
@@ -1646,6 +1648,7 @@ qnf4_status multi_bwd(const BaseSrc& src, const Adapters& ad, const void* x, con
   if (!ws || ws_bytes < P.total) return fail(QNF4_ERR_WORKSPACE, "workspace too small (%zu < %zu)", ws_bytes, P.total);
   if (!al16(ws)) return fail(QNF4_ERR_ALIGN, "the workspace must be 16-byte aligned");
   BufList out, in;
+  out.add(ws, static_cast<int64_t>(P.total), 1);
   out.add(dX, M * K, 2);
   out.add(dA, ad.n * ad.r * K, sizeof(float));
   out.add(dB, ad.n * N * ad.r, sizeof(float));

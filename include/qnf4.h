@@ -360,8 +360,8 @@ QNF4_API qnf4_status qnf4_loftq_nf4(const void* W_bf16, int64_t N, int64_t K, in
  * 0 .. n - 1 (e.g. -1) means no adapter, the base product alone. A [n, r, K] and B [n, N, r]
  * bf16 (adapters of a lower rank are padded with zero rows of A), scales fp32 [n], all on the
  * device. An adapter that holds infinities or NaNs reaches its own tokens only. No output
- * overlaps an input, another output or the workspace (here and in the calls below; one over
- * an input or another output is refused, QNF4_ERR_ARG, in a group over any layer's). Other
+ * overlaps an input, another output or the workspace (here and in the calls below;
+ * QNF4_ERR_ARG, in a group over any layer's buffer). Nor does the workspace an input. Other
  * arguments, checks and limits as in qnf4_qlora_linear_fwd; M = 0 is a no-op. Workspace:
  * qnf4_multi_workspace_size(QNF4_OP_FWD, N, K, M, n, r). */
 QNF4_API size_t qnf4_multi_workspace_size(int32_t op, int64_t N, int64_t K, int64_t M, int32_t n,

@@ -34,3 +34,24 @@ def test_grouped_outputs_over_and_beside_other_buffers():
     with pytest.raises((ValueError, q.Qnf4Error), match="overlaps"):
         q.qlora_linear_multi_fwd_group(ws_[::-1], xs[::-1], ids, As[::-1], Bs[::-1], s, hs=[over[: M * 64].view(M, 64), hs[0]])
     q.check()
+
+
+@pytest.mark.parametrize("M", [4, 40, 900])
+def test_workspaces_over_and_beside_other_buffers(M):
+    import bit_nf4_quantized_04_b200 as q
+    N, K, n, r = 128, 192, 3, 4
+    ids = multi_ref.make_ids("tokens", M, n, 910, "cuda")
+    s = torch.ones(n, device="cuda")
+    w = q.quantize_weight(synth.llama_weight((N, K), 911, device="cuda"))
+    A, B = synth.normal_bf16((n, r, K), 0.05, 912, "cuda"), synth.normal_bf16((n, N, r), 0.05, 913, "cuda")
+    need = q.multi_workspace_size(q._lib.OP_FWD, N, K, M, n, r)
+    room = torch.zeros(need + 2 * M * K, dtype=torch.uint8, device="cuda")
+    x = room[need:].view(torch.bfloat16).view(M, K)  # right behind the workspace
+    x.copy_(synth.normal_bf16((M, K), 1.0, 914, "cuda"))
+    want = q.qlora_linear_multi_fwd(w, x.clone(), ids, A, B, s)
+    assert torch.equal(q.qlora_linear_multi_fwd(w, x, ids, A, B, s, ws=room[:need]), want)
+    over = torch.zeros(max(need, 2 * M * K), dtype=torch.uint8, device="cuda")
+    xo = over[: 2 * M * K].view(torch.bfloat16).view(M, K)
+    with pytest.raises((ValueError, q.Qnf4Error), match="overlaps"):
+        q.qlora_linear_multi_fwd(w, xo, ids, A, B, s, ws=over)
+    q.check()

@@ -90,3 +90,21 @@ def test_a_grouped_output_over_any_layers_buffer_is_refused(q, layers):
             ls = [Buffers(q, 4, 16 * i) for i in range(layers)]
             ls[0].h = getattr(ls[at], other)
             assert _group(q, ls, 3, 8) == ERR_ARG, (other, at)
+
+
+@pytest.mark.parametrize("M", [1, 16, 100, 1000])
+@pytest.mark.parametrize("fn", ["qlora_linear_multi_fwd", "dense_linear_multi_fwd", "qlora_linear_multi_bwd",
+                                "dense_linear_multi_bwd"])
+def test_a_workspace_over_another_buffer_is_refused(q, fn, M):
+    for other in READ[fn[:5]].split() + (["dY", "dX", "dA", "dB"] if fn.endswith("bwd") else ["h"]):
+        b = Buffers(q, M)
+        b.ws = getattr(b, other)
+        assert b.call(fn) == ERR_ARG, other
+
+
+def test_a_groups_workspace_over_any_layers_buffer_is_refused(q):
+    for other in READ["qlora"].split() + ["h"]:
+        for at in range(3) if other not in ("ids", "s") else (0,):
+            ls = [Buffers(q, 4, 16 * i) for i in range(3)]
+            ls[0].ws = getattr(ls[at], other)
+            assert _group(q, ls, 3, 8) == ERR_ARG, (other, at)
