@@ -1763,6 +1763,24 @@ qnf4_status check_grad_outputs(int32_t count, const void* const* g, const int32_
   return QNF4_OK;
 }
 
+// The norms and the workspace lie apart from each other and from every gradient and output.
+qnf4_status check_grad_apart(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
+                             int32_t n, void* const* out, const float* norm, const void* ws, size_t need) {
+  const uintptr_t nb = reinterpret_cast<uintptr_t>(norm), ne = nb + static_cast<uintptr_t>(n) * sizeof(float);
+  const uintptr_t wb = reinterpret_cast<uintptr_t>(ws), we = wb + need;
+  if (nb < we && wb < ne) return fail(QNF4_ERR_ARG, "norm overlaps the workspace");
+  for (int32_t t = 0; t < count; ++t) {
+    const uintptr_t bytes = static_cast<uintptr_t>(elems[t]) * (dtype[t] == QNF4_OUT_BF16 ? 2 : 4);
+    if (!bytes) continue;
+    for (const void* p : {g[t], out ? static_cast<const void*>(out[t]) : g[t]}) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p), end = at + bytes;
+      if ((at < ne && nb < end) || (at < we && wb < end))
+        return fail(QNF4_ERR_ARG, "norm or the workspace overlaps tensor %d", t);
+    }
+  }
+  return QNF4_OK;
+}
+
 qnf4_status check_grad_args(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
                             int32_t n, void* const* out, const float* norm) {
   if (count < 0) return fail(QNF4_ERR_ARG, "count must be >= 0 (got %d)", count);
@@ -1809,9 +1827,11 @@ template <int CAP>
 qnf4_status grad_norm_clip_in(int32_t count, const void* const* g, const int32_t* dtype, const int64_t* elems,
                            int32_t n, float max_norm, void* const* out, float* norm, void* ws,
                            size_t ws_bytes, cudaStream_t s) {
-  if (!ws || !al16(ws) || ws_bytes < grad_ws_bytes(count, elems, n))
-    return fail(QNF4_ERR_WORKSPACE, "workspace too small or not 16-byte aligned (%zu < %zu)", ws_bytes,
-                grad_ws_bytes(count, elems, n));
+  const size_t need = grad_ws_bytes(count, elems, n);
+  if (!ws || !al16(ws) || ws_bytes < need)
+    return fail(QNF4_ERR_WORKSPACE, "workspace too small or not 16-byte aligned (%zu < %zu)", ws_bytes, need);
+  const qnf4_status st = check_grad_apart(count, g, dtype, elems, n, out, norm, ws, need);
+  if (st != QNF4_OK) return st;
   const int64_t pieces = grad_pieces(count, elems, n);
   double* sums = static_cast<double*>(ws);
   float* coef = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +

@@ -414,8 +414,9 @@ QNF4_API qnf4_status qnf4_dense_linear_multi_bwd(const void* W_bf16, int64_t N, 
  * The squares are summed in float64 and in a fixed order, so no finite gradient overflows on
  * the way and equal calls give equal bits. g, dtype and elems are host arrays of `count`
  * entries (0 gives norms of 0); the tensors need only be aligned to their element size.
- * Workspace: qnf4_grad_workspace_size(count, elems, n). Errors: QNF4_ERR_ARG for NULL or a
- * dtype other than the two, QNF4_ERR_SHAPE where elems[t] is not a multiple of n. */
+ * Workspace: qnf4_grad_workspace_size(count, elems, n). norm and the workspace overlap neither
+ * each other nor a tensor. Errors: QNF4_ERR_ARG for NULL, for such an overlap or a dtype other
+ * than the two, QNF4_ERR_SHAPE where elems[t] is not a multiple of n. */
 QNF4_API size_t qnf4_grad_workspace_size(int32_t count, const int64_t* elems, int32_t n);
 QNF4_API qnf4_status qnf4_grad_norm(int32_t count, const void* const* g, const int32_t* dtype,
                            const int64_t* elems, int32_t n, float* norm, void* ws,

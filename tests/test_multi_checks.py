@@ -108,3 +108,25 @@ def test_a_groups_workspace_over_any_layers_buffer_is_refused(q):
             ls = [Buffers(q, 4, 16 * i) for i in range(3)]
             ls[0].ws = getattr(ls[at], other)
             assert _group(q, ls, 3, 8) == ERR_ARG, (other, at)
+
+
+@pytest.mark.parametrize("clip", [False, True])
+def test_norms_and_workspaces_over_gradients_are_refused(q, clip):
+    # two gradients of 4096 fp32 and 4096 bf16, 4 adapters, scaled into buffers of their own
+    g, out, norm, ws = (FAKE, 2 * FAKE), (3 * FAKE, 4 * FAKE), 5 * FAKE, 6 * FAKE
+    elems = (C.c_int64 * 2)(4096, 4096)
+    need = q.lib.qnf4_grad_workspace_size(2, C.addressof(elems), 4)
+
+    def f(norm=norm, ws=ws):
+        p, o, dt = (C.c_void_p * 2)(*g), (C.c_void_p * 2)(*out), (C.c_int32 * 2)(0, 1)
+        a = (2, C.addressof(p), C.addressof(dt), C.addressof(elems), 4)
+        if clip:
+            return q.lib.qnf4_clip_grad_norm(*a, 1.0, C.addressof(o), norm, ws, need, None)
+        return q.lib.qnf4_grad_norm(*a, norm, ws, need, None)
+
+    tensors = [(g[0], 4 * 4096), (g[1], 2 * 4096)] + ([(out[0], 4 * 4096), (out[1], 2 * 4096)] if clip else [])
+    for at, size in tensors:
+        for p in (at, at + size - 16):
+            assert f(norm=p) == ERR_ARG and f(ws=p) == ERR_ARG
+        assert f(ws=at - need + 16) == ERR_ARG
+    assert f(norm=ws) == ERR_ARG and f(norm=ws + need - 16) == ERR_ARG
