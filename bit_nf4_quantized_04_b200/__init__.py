@@ -467,9 +467,15 @@ def _raw_stream(t: torch.Tensor) -> int:
 
 
 @lru_cache(maxsize=4096)
-def multi_workspace_size(op: int, N: int, K: int, M: int, n: int, r: int) -> int:
-    """Workspace bytes of a many-adapter call (op: OP_FWD or OP_BWD)."""
+def _multi_ws_size(device: int, op: int, N: int, K: int, M: int, n: int, r: int) -> int:
+    # the plan, and with it the size, depends on how many SMs the (current) device has
     return int(lib.qnf4_multi_workspace_size(op, N, K, M, n, r))
+
+
+def multi_workspace_size(op: int, N: int, K: int, M: int, n: int, r: int) -> int:
+    """Workspace bytes of a many-adapter call on the current device (op: OP_FWD or OP_BWD)."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    return _multi_ws_size(device, op, N, K, M, n, r)
 
 
 _BF16 = torch.bfloat16
@@ -564,7 +570,7 @@ def _multi_fwd(fn: str, base, bts, N, K, x, ids, A, B, scales, h, ws):
     if M == 0:
         return h
     with _on(x):
-        wsb, size = _multi_ws(multi_workspace_size(_lib.OP_FWD, N, K, M, n, r), x, ws)
+        wsb, size = _multi_ws(_multi_ws_size(x.get_device(), _lib.OP_FWD, N, K, M, n, r), x, ws)
         _lib.call(fn, *base, x.data_ptr(), M, ids.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
                   scales.data_ptr(), h.data_ptr(), wsb.data_ptr(), size, _raw_stream(x))
     return h
@@ -583,7 +589,7 @@ def _multi_bwd(fn: str, base, bts, N, K, x, dY, ids, A, B, scales, dX, dA, dB, w
         dB.zero_()
         return dX, dA, dB
     with _on(x):
-        wsb, size = _multi_ws(multi_workspace_size(_lib.OP_BWD, N, K, M, n, r), x, ws)
+        wsb, size = _multi_ws(_multi_ws_size(x.get_device(), _lib.OP_BWD, N, K, M, n, r), x, ws)
         _lib.call(fn, *base, x.data_ptr(), dY.data_ptr(), M, ids.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
                   scales.data_ptr(), dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), wsb.data_ptr(), size,
                   _raw_stream(x))
@@ -642,7 +648,8 @@ def qlora_linear_multi_fwd_group(ws_: list, xs: list, ids: torch.Tensor, As: lis
         hs = [_multi_out(h, (M, w.N), torch.bfloat16, "h", xs[0]) for w, h in zip(ws_, hs, strict=True)]
     ptrs = lambda ts: (C.c_void_p * k)(*[t.data_ptr() for t in ts])  # noqa: E731
     with _on(xs[0]):
-        wsb, size = _multi_ws(sum([multi_workspace_size(_lib.OP_FWD, w.N, w.K, M, n, r) for w in ws_]), xs[0], ws)
+        d = xs[0].get_device()
+        wsb, size = _multi_ws(sum([_multi_ws_size(d, _lib.OP_FWD, w.N, w.K, M, n, r) for w in ws_]), xs[0], ws)
         _lib.call("qnf4_qlora_linear_multi_fwd_group", k, (_lib.Qnf4Weight * k)(*[w.c() for w in ws_]), ptrs(xs), M,
                   ids.data_ptr(), n, ptrs(As), ptrs(Bs), r, scales.data_ptr(), ptrs(hs), wsb.data_ptr(), size,
                   _raw_stream(xs[0]))

@@ -130,3 +130,15 @@ def test_norms_and_workspaces_over_gradients_are_refused(q, clip):
             assert f(norm=p) == ERR_ARG and f(ws=p) == ERR_ARG
         assert f(ws=at - need + 16) == ERR_ARG
     assert f(norm=ws) == ERR_ARG and f(norm=ws + need - 16) == ERR_ARG
+
+
+def test_workspace_sizes_are_each_devices_own(q, monkeypatch):
+    # the library's answer depends on the current device's SMs: one that was asked on another device
+    # is asked again
+    sms, now = {0: 148, 1: 132}, [0]
+    monkeypatch.setattr(q.torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(q.torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(q.lib, "qnf4_multi_workspace_size", lambda op, N, K, M, n, r: N * sms[now[0]])
+    for d in (0, 1, 0, 1):
+        now[0] = d
+        assert q.multi_workspace_size(q._lib.OP_FWD, 123456, 64, 77, 3, 8) == 123456 * sms[d]
