@@ -549,6 +549,8 @@ def _multi_ws(need: int, like: torch.Tensor, ws):
     _ws(need, like, ws)
     if ws.get_device() != like.get_device():
         raise ValueError("the workspace must be on the tensors' device")
+    if not ws.is_contiguous():  # (its elements' bytes would not be what lies behind its address)
+        raise ValueError("the workspace must be contiguous")
     return ws, ws.numel() * ws.element_size()
 
 

@@ -3,6 +3,7 @@ nothing is launched."""
 import ctypes as C
 
 import pytest
+import torch
 
 FAKE = 1 << 20  # never dereferenced
 BIG = 1 << 40
@@ -142,3 +143,12 @@ def test_workspace_sizes_are_each_devices_own(q, monkeypatch):
     for d in (0, 1, 0, 1):
         now[0] = d
         assert q.multi_workspace_size(q._lib.OP_FWD, 123456, 64, 77, 3, 8) == 123456 * sms[d]
+
+
+def test_workspaces_that_are_not_contiguous_are_refused(q):
+    # 64 elements in one byte, or in every second one
+    like, room = torch.zeros(4), torch.zeros(128, dtype=torch.uint8)
+    for ws in (room[:1].expand(64), room[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            q._multi_ws(32, like, ws)
+    assert q._multi_ws(32, like, room[64:])[1] == 64
