@@ -67,8 +67,9 @@ qnf4_status launched(const char* what, int n = 1) {
 }
 
 // Launch as a programmatic dependent of the previous kernel in the stream: the kernel
-// may start (and run its prologue) while that kernel finishes; every kernel launched
-// this way calls griddepcontrol.wait before it touches global memory.
+// may start (and run its prologue) while that kernel finishes. Every kernel launched this way
+// calls griddepcontrol.wait before it touches what the grid before it may still write or read,
+// and at the latest before it ends (which of them read anything earlier: see k_gemm).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {
@@ -1199,9 +1200,16 @@ struct MultiPlan {
 
 // Product for many tokens (multi_mm.cuh) or k_gemm's? The former costs writing the base in 16
 // bits and tiles of 256 tokens; its output rows must be 16-byte aligned, and its copies of the
-// adapters stay below the base's size.
-// (measured, 8 adapters of r = 16 through 4096 x 4096, k_gemm against this: forward NF4 43 / 52 us at
-// 512 tokens, 54 / 53 at 1024; bf16 41 / 44, 50 / 45; backward NF4 68 / 72, 86 / 75)
+// adapters stay below the base's size. Measured, k_gemm against this, us, 8 adapters of r = 16 (tokens
+// in runs; the whole call):
+//   forward NF4   4096 x 4096   43 / 49 at 512 tokens, 49 / 52 at 767, 56 / 53 at 1024
+//                 4096 x 11008  76 / 100, 101 / 104, 112 / 106     (features x contraction)
+//                 11008 x 4096  92 / 83, 95 / 89, 131 / 104
+//   forward bf16  4096 x 4096   40 / 42, 43 / 44, 49 / 45;  11008 x 4096  91 / 62, 86 / 68, 119 / 83
+//   backward NF4  4096 x 4096   68 / 68, 83 / 71, 87 / 75;  11008 x 4096 122 / 137, 167 / 142, 173 / 144
+// One threshold for all: it is right within a fifth over an NF4 base. It is not where the base is 16-bit
+// and wide: from 257 tokens on (more tiles than SMs) k_gemm's cut last wave loses to this by up to a half
+// (384 tokens: 90 / 61).
 constexpr int64_t kMmMinTokens = 768;
 bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
   return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K) &&
@@ -1428,7 +1436,6 @@ qnf4_status multi_main(const BaseSrc& src, int main_src, const MultiPlan& P, con
   g.mt_list = reinterpret_cast<const int*>(w8 + P.off_list);
   g.mt_ids = ad.ids;
   g.mt_exp = exp;
-  g.mt_n = ad.n;
   g.mt_dmax = P.dmax;
   g.mt_cmax = P.cmax;
   g.mt_per = P.per;

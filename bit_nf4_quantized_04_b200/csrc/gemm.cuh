@@ -157,7 +157,7 @@ struct GemmArgs {
   const int* mt_ids;      // [cols] the tokens' adapters
   const uint16_t* mt_exp; // Bext [column tiles][mt_cmax][tn][64]
   int64_t ext_as;
-  int mt_n, mt_dmax, mt_cmax, mt_per, mt_r16;
+  int mt_dmax, mt_cmax, mt_per, mt_r16;
   int clus;               // > 1: no whole waves, and a tile's slices are the CTAs of a cluster
   int lazy_dep;           // programmatic dependent launch: 0 = every thread waits for the
                           // previous grid after the prologue; 1 = only the adapter chunk's
@@ -578,9 +578,13 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // Programmatic dependent launch: the prologue above overlapped the previous grid.
-  // Every kernel of the library waits for its predecessor before it lets its own
-  // dependents start, so a dependent may read anything older than its predecessor.
+  // Programmatic dependent launch: the prologue above overlapped the previous grid. With
+  // lazy_dep this grid also reads before its wait what grids older than the previous one
+  // wrote. That holds because the previous grid (the u kernel, the projections, the
+  // gradients) itself waits before it lets this one start. Three kernels do not: k_gemm
+  // with lazy_dep, k_multi_prep with lazy, and k_multi_mm. Whatever is launched after one
+  // of those must wait before its first access; the first kernel of every call does, and
+  // the projections do after k_multi_prep.
   if (!g.lazy_dep) griddep_wait();
   griddep_launch_dependents();
 

@@ -113,8 +113,9 @@ QNF4_DEV void bf16_parts(float v, uint16_t (&h)[3]) {
 // the CTA finds them out; X and the adapters' rows therefore have rings of their own, from either
 // end of one buffer, of as many steps as fit once the number of slots is known.
 //
-// Outputs: the main product's operand blocks (bf16 s u, zeros in the other slots), the tile's
-// list of adapters, and for the gradients the values in three bf16 parts that add up to the
+// Outputs: the main product's operand blocks (bf16 s u, zeros in the other slots; the rounding, at
+// most 2^-8 of s u, is the one-adapter layer's too, and a second bf16 part would be rp more columns of
+// the product for every adapter of a tile), the tile's list of adapters, and for the gradients the values in three bf16 parts that add up to the
 // fp32 value (bf16_parts), transposed to [3 r16][sorted token].
 constexpr int kFlushSteps = 4;
 constexpr uint32_t kProjRing = 104u * 1024u;
@@ -504,6 +505,9 @@ __global__ void __launch_bounds__(kMultiThreads, 2) k_multi_proj(const __grid_co
 // [n, N, r] into BT [n, r, N], clear the projections' parts and the counters. Bound by the latency
 // of CTA 0's passes over the ids: 6 us for 4096 tokens of 4 adapters, 10 us for 8192 of 8 (one CTA
 // keeps the sort free of a grid-wide barrier; by many tokens it runs under the stage kernel's end).
+// Up to 4096 tokens only named adapters are transposed, at a pass over the ids for each 64 rows of each
+// adapter: nothing for a few, but with 4096 adapters of r = 16 and N = 11008, 8 of them named by 64
+// tokens, most of a backward call of 4.2 ms (writing dB's zeros takes 0.45).
 struct GradSlice {
   int a, p0, steps;
   int count;   // slices of this adapter

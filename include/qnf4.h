@@ -172,8 +172,9 @@ QNF4_API qnf4_status qnf4_double_quant_shard(const float* absmax, int64_t nb1, i
 
 /* [QLoRA opening formula, 贡献二] Two-level dequantization of a whole weight to
  * out [N, K] as fp32 (out_dtype QNF4_OUT_F32) or bf16 round-to-nearest-even
- * (QNF4_OUT_BF16). Meant for tests and export: the linear layer never writes the
- * dequantized weight to memory. */
+ * (QNF4_OUT_BF16). Meant for tests and export: the one-adapter linear layer never writes the
+ * dequantized weight to memory (the many-adapter calls of 768 tokens and more write it to their
+ * workspace, in bf16, for the length of the call). */
 QNF4_API qnf4_status qnf4_dequant(const qnf4_weight* w, void* out, int32_t out_dtype, void* stream);
 
 /* [QLoRA opening formula] h = x * bf16(W_hat)^T + scale * (x A^T) B^T, with W_hat
@@ -356,14 +357,23 @@ QNF4_API qnf4_status qnf4_loftq_nf4(const void* W_bf16, int64_t N, int64_t K, in
 /* [QLoRA opening formula, for the adapters of many requests at once] The linear layer with
  * n (1..4096) adapters over one frozen base, each token using its own:
  *   h[m] = x[m] bf16(W_hat)^T + scales[a] (x[m] A[a]^T) B[a]^T,   a = ids[m],
- * h [M, N] bf16, fp32 accumulation, one rounding. ids int32 [M] in any order; an id outside
- * 0 .. n - 1 (e.g. -1) means no adapter, the base product alone. A [n, r, K] and B [n, N, r]
- * bf16 (adapters of a lower rank are padded with zero rows of A), scales fp32 [n], all on the
- * device. An adapter that holds infinities or NaNs reaches its own tokens only. No output
- * overlaps an input, another output or the workspace (here and in the calls below;
- * QNF4_ERR_ARG, in a group over any layer's buffer). Nor does the workspace an input. Other
- * arguments, checks and limits as in qnf4_qlora_linear_fwd; M = 0 is a no-op. Workspace:
- * qnf4_multi_workspace_size(QNF4_OP_FWD, N, K, M, n, r). */
+ * h [M, N] bf16, fp32 accumulation. ids int32 [M] in any order; an id outside 0 .. n - 1
+ * (e.g. -1) means no adapter, the base product alone. A [n, r, K] and B [n, N, r] bf16
+ * (adapters of a lower rank are padded with zero rows of A), scales fp32 [n], all on the
+ * device. An adapter that holds infinities or NaNs reaches its own tokens only.
+ * Roundings: h, once. s u = scales[a] x[m] A[a]^T to bf16 between its two products, as in the
+ * one-adapter calls, except at 1..16 tokens over an NF4 weight, where it stays in fp32. W_hat
+ * once, but with few tokens its parts instead: bf16(level) with an fp32 constant at 1..16 tokens,
+ * bf16(bf16(level) bf16(constant)) at 17..32 (and for dX up to 32). So a token's result depends,
+ * within these roundings, on how many tokens came with it.
+ * No output overlaps an input, another output or the workspace, and the workspace no input
+ * (QNF4_ERR_ARG, here and in the calls below; in a group over any layer's buffer). Other
+ * arguments, checks and limits as in qnf4_qlora_linear_fwd; M = 0 is a no-op.
+ * Workspace: qnf4_multi_workspace_size(QNF4_OP_FWD, N, K, M, n, r). From 768 tokens on most of it
+ * is bf16(W_hat) of an NF4 weight, 2 N K bytes, and the tokens' s u, 2 M min(n, 256) rp bytes (rp: r
+ * padded to 16, 32 or 64); with fewer tokens, or where n rp is above K, the s u in 128 M c bytes,
+ * c = min(n, 256) / floor(64 / r16) rounded up (r16: r padded to a multiple of 16). Both are for as
+ * many adapters as a tile of 256 tokens can name, not for those that it does. */
 QNF4_API size_t qnf4_multi_workspace_size(int32_t op, int64_t N, int64_t K, int64_t M, int32_t n,
                                  int32_t r);
 QNF4_API qnf4_status qnf4_qlora_linear_multi_fwd(const qnf4_weight* w, const void* x, int64_t M,
@@ -389,9 +399,11 @@ QNF4_API qnf4_status qnf4_qlora_linear_multi_fwd_group(int32_t k, const qnf4_wei
 
 /* Its backward, given dY [M, N] bf16: per token (a = ids[m], v[m] = scales[a] dY[m] B[a],
  * u[m] = scales[a] x[m] A[a]^T, both 0 without an adapter)
- *   dX[m] = dY[m] bf16(W_hat) + v[m] A[a]      bf16 [M, K]
+ *   dX[m] = dY[m] bf16(W_hat) + v[m] A[a]      bf16 [M, K]    (v rounded to bf16, here only)
  *   dA[a] = sum of v[m]^T x[m]                 fp32 [n, r, K]  over the tokens of adapter a
  *   dB[a] = sum of dY[m]^T u[m]                fp32 [n, N, r]
+ * An infinity or a NaN in x or dY reaches its own token and adapter only, and gives there what
+ * IEEE sums of the formula give (beside finite adapters).
  * dA and dB are written, not accumulated, with zeros for an adapter without tokens (and for
  * M = 0). N must be a multiple of 8. Workspace: qnf4_multi_workspace_size(QNF4_OP_BWD, ...). */
 QNF4_API qnf4_status qnf4_qlora_linear_multi_bwd(const qnf4_weight* w, const void* x, const void* dY,
