@@ -1203,13 +1203,16 @@ struct MultiPlan {
 // adapters stay below the base's size. Measured, k_gemm against this, us, 8 adapters of r = 16 (tokens
 // in runs; the whole call):
 //   forward NF4   4096 x 4096   43 / 49 at 512 tokens, 49 / 52 at 767, 56 / 53 at 1024
-//                 4096 x 11008  76 / 100, 101 / 104, 112 / 106     (features x contraction)
+//                 4096 x 11008  76 / 100, 101 / 104, 112 / 106     (N x K)
 //                 11008 x 4096  92 / 83, 95 / 89, 131 / 104
 //   forward bf16  4096 x 4096   40 / 42, 43 / 44, 49 / 45;  11008 x 4096  91 / 62, 86 / 68, 119 / 83
 //   backward NF4  4096 x 4096   68 / 68, 83 / 71, 87 / 75;  11008 x 4096 122 / 137, 167 / 142, 173 / 144
-// One threshold for all: it is right within a fifth over an NF4 base. It is not where the base is 16-bit
+// One threshold for all: it is right within a quarter over an NF4 base. It is not where the base is 16-bit
 // and wide: from 257 tokens on (more tiles than SMs) k_gemm's cut last wave loses to this by up to a half
 // (384 tokens: 90 / 61).
+// The bound on the copies, over NF4 4096 x 4096, forward: 1024 adapters of r = 16, tokens in runs, 116 / 197
+// at 1024 tokens, 322 / 390 at 4096; 256 of r = 64 266 / 219, 466 / 322, and 2500 / 1438 where each of 4096
+// tokens draws its own. Right for r = 16, not for 64; backward the two are within a tenth.
 constexpr int64_t kMmMinTokens = 768;
 bool use_mm(int64_t N, int64_t K, int64_t M, int n, int rp, bool bwd) {
   return M >= kMmMinTokens && N % 8 == 0 && static_cast<int64_t>(n) * rp <= (bwd ? N : K) &&
