@@ -44,7 +44,7 @@
 //
 // Roles (64 + 128 NSET threads): warp 0 issues TMA, warp 1 allocates TMEM and one
 // lane issues tcgen05.mma, and NSET sets of four "converter" warps dequantize (set h
-// takes the steps i with i % NSET == h, one 64-element NF4 block per thread and
+// takes every NSET-th ring position, one 64-element NF4 block per thread and
 // step) and then run the epilogue (tcgen05.ld from TMEM, optional split-K reduction
 // in the last-arriving CTA). For A_NF4_K the dequantized operand goes straight into
 // tensor memory with tcgen05.st and the MMA reads A from there (likewise for
@@ -464,16 +464,19 @@ __device__ __noinline__ float ext_fix(const GemmArgs& g, int64_t row, int64_t co
 // Where a converter set's step sits in the two rings, advanced without division
 // (NSET <= S2 <= S1, so an index wraps at most once per advance). Both rings advance
 // once per position, over all units of the CTA: a unit's contraction steps, then its
-// adapter chunk. i = position in the unit, r = ring position, s / ph = load-ring slot
+// adapter chunk. A set takes the ring positions r with r % NSET == set, through all units:
+// that its positions are NSET apart everywhere is what makes its waits exact (see acquire).
+// i = position in the unit, r = ring position, s / ph = load-ring slot
 // and phase, s2 = A stage; sj / phj = load-ring slot and phase of position r - S2,
 // the last user of that A stage (valid once r >= S2): the MMA's release of that slot
 // also releases the stage.
 struct ConvCursor {
   int i, r, s, s2, sj;
   uint32_t ph, phj;
-  QNF4_DEV ConvCursor(int set, int rbase, int S1, int S2) {
-    i = set;
-    r = rbase + set;
+  // (first: the set's first position in the unit that starts at ring position rbase)
+  QNF4_DEV ConvCursor(int first, int rbase, int S1, int S2) {
+    i = first;
+    r = rbase + first;
     s = r % S1;
     ph = static_cast<uint32_t>(r / S1) & 1u;
     s2 = r % S2;
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
   } else {
     // ------------------------------------------------------------ converters
     const int ct = threadIdx.x - 64;  // 0 .. NCONV-1
-    const int set = ct >> 7;          // converter set: steps i with i % NSET == set
+    const int set = ct >> 7;          // converter set: ring positions r with r % NSET == set
     const int t = ct & 127;           // row slot 0..127
     const int q = warp & 3;           // TMEM lane quarter this warp may access
     const int lrow = q * 32 + lane;   // the accumulator row (TMEM lane) of this thread
@@ -1095,26 +1098,31 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     float snext = 0.f;
     int64_t bstep = 0;
     int cn = 0;  // MN-major: contraction index (weight row) of the next step's block
-    // block index of this slot's first step in unit w
-    auto first_block = [&](const Unit& w) -> int64_t {
+    int rbase = 0;  // ring position of the current unit's first step
+    // this set's first position in a unit that starts at ring position rb
+    auto first_of = [&](int rb) { return NSET == 1 ? 0 : (set + NSET - rb % NSET) % NSET; };
+    // block index of this slot's first step, `first`, in unit w
+    auto first_block = [&](const Unit& w, int first) -> int64_t {
       if (ASRC == A_NF4_K) {
         const int64_t n = w.row0 + slot;
         rowok = n < g.wN;
-        return n * g.nbk + w.step0 + set;
+        return n * g.nbk + w.step0 + first;
       }
       const int kb = slot >> 6, nr = slot & 63;
       const int64_t kblk = w.row0 / 64 + kb;
       rowok = kblk < g.nbk;
-      cn = (w.step0 + set) * kStep + nr;
-      return (static_cast<int64_t>(w.step0 + set) * kStep + nr) * g.nbk + kblk;
+      cn = (w.step0 + first) * kStep + nr;
+      return (static_cast<int64_t>(w.step0 + first) * kStep + nr) * g.nbk + kblk;
     };
-    // constants of this set's first step in unit un (none past the last unit)
-    auto prefetch_unit = [&](int un) {
+    // constants of this set's first step in unit un, which starts at ring position rb (none
+    // past the last unit)
+    auto prefetch_unit = [&](int un, int rb) {
       vnext = false;
       if (un < g.nunits) {
         const Unit wn = unit_of<MULTI>(g, un);
-        bnext = first_block(wn);
-        vnext = rowok && set < wn.nst && (ASRC == A_NF4_K || cn < g.wN);
+        const int first = first_of(rb);
+        bnext = first_block(wn, first);
+        vnext = rowok && first < wn.nst && (ASRC == A_NF4_K || cn < g.wN);
       }
       if (vnext && !in_bounds(bnext < g.cst_elems, 27)) vnext = false;
       if (vnext) {
@@ -1141,10 +1149,10 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       mu = *g.mean;
       bstep = (ASRC == A_NF4_K) ? static_cast<int64_t>(NSET)
                                 : static_cast<int64_t>(NSET) * kStep * g.nbk;
-      prefetch_unit(u0);
+      prefetch_unit(u0, 0);
     } else if constexpr (ASRC == A_CHANQ_MN) {
       bstep = static_cast<int64_t>(NSET) * kStep * g.nbk;
-      prefetch_unit(u0);
+      prefetch_unit(u0, 0);
     } else if constexpr (ASRC == A_CHANQ_K) {
       if (set == 0) {
         uint32_t* t1 = reinterpret_cast<uint32_t*>(base + sp.cq);
@@ -1175,13 +1183,16 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
       }
       mbar_arrive(&full2[cur.s2]);
     };
-    // Wait until step cur's packed data has landed and its A stage is free (the MMA
-    // of the position S2 earlier has completed).
+    // Wait until step cur's A stage is free (the MMA of the position S2 earlier has
+    // completed) and its packed data has landed. A test of a phase's parity is also true one
+    // phase too early, so each wait needs to know that the slot's previous phase is complete:
+    // this set waited for the MMA of position r - NSET - S2 before, which is at or past
+    // r - S2 - S1 (NSET <= S1); and the MMA of r - S2, once waited for, is at or past the
+    // landing of r - S1. Hence this order, and positions NSET apart in every unit.
     auto acquire = [&](const ConvCursor& cur, unsigned int site) -> bool {
-      if (!wait_or_abort(&full1[cur.s], cur.ph, g.wait_ns, &s_abort, site)) return false;
       if (cur.r >= S2 && !wait_or_abort(&empty1[cur.sj], cur.phj, g.wait_ns, &s_abort, site + 1))
         return false;
-      return true;
+      return wait_or_abort(&full1[cur.s], cur.ph, g.wait_ns, &s_abort, site);
     };
     // The adapter position writes no A stage, but its full2 arrival must fall in that
     // stage's next phase: wait for the stage's previous user as a conversion would.
@@ -1214,7 +1225,7 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
             }
           }
         } else {
-          prefetch_unit(u + ustep);
+          prefetch_unit(u + ustep, rbase + w.nst + w.nx);
         }
         if (!acquire(cur, 31)) return false;
         const uint8_t* pk = base + cur.s * sp.slot1 + sp.off_p1;
@@ -1317,20 +1328,19 @@ __global__ void __launch_bounds__(gemm_threads(NSET), MINB)
     // of unit k-1 (those steps wait only for MMAs of earlier units), so the MMA has
     // work the moment the accumulator is free again.
     const int ahead = min(NSET, S2);
-    int rbase = 0;  // ring position of the unit's first step
-    int up = -1;    // the previous unit, while its epilogue is still due
+    int up = -1;  // the previous unit, while its epilogue is still due
     // One pass per unit of this CTA and a last one for the final epilogue; the
     // epilogue and the adapter write each have a single call site (smaller code).
     for (int k = 0;; ++k) {
       const int u = u0 + k * ustep;
       const bool live = u < g.nunits;  // a unit to convert (else only the last epilogue)
       // (dense sources have no A ring: the cursor gets a dummy depth)
-      ConvCursor cur(set, rbase, S1, DEQ ? S2 : 1);
+      ConvCursor cur(first_of(rbase), rbase, S1, DEQ ? S2 : 1);
       if (live) {
         const Unit w = unit_of<MULTI>(g, u);
         unit_rows(w);
         if constexpr (ASRC == A_NF4_K || ASRC == A_NF4_MN || ASRC == A_CHANQ_MN) {
-          if (set >= w.nst) prefetch_unit(u + ustep);  // no step of this set here
+          if (cur.i >= w.nst) prefetch_unit(u + ustep, rbase + w.nst + w.nx);  // no step of this set here
         }
         // positions converted before the previous unit's epilogue
         if (DEQ && up >= 0 && !dead) {

@@ -85,6 +85,26 @@ def test_whole_tiles_beside_a_cut_last_wave(case, kind):
     _check(q, kind, K, N, *rest, 820, ops=("bwd",))
 
 
+@pytest.mark.parametrize("N,K,M,n,r", [(5120, 13824, 300, 64, 64), (4096, 11008, 500, 64, 16), (4160, 11008, 500, 50, 64),
+                                       (4224, 11008, 500, 40, 33), (11008, 4096, 500, 64, 16), (13824, 5120, 300, 64, 64)])
+@pytest.mark.parametrize("kind", ["nf4", "dense"])
+def test_many_chunks_between_the_tiles_of_a_cta(kind, N, K, M, n, r):
+    # adapter chunks are short steps beside the base's: a CTA's converters run far ahead of the loads
+    # where one tile's chunks end and the next tile's base begins, for several remainders of the tiles'
+    # steps by the number of converter sets; twenty calls, equal bits, the first within its bounds
+    import bit_nf4_quantized_04_b200 as q
+    x, A, B, dY, ids, s = _inputs(N, K, M, n, r, "tokens", 850)
+    base, What, fwd, bwd = _base(q, kind, synth.llama_weight((N, K), 850, device="cuda"))
+    W = What.bfloat16()
+    first = [fwd(base, x, ids, A, B, s), *bwd(base, x, dY, ids, A, B, s)]
+    for _ in range(20):
+        again = [fwd(base, x, ids, A, B, s), *bwd(base, x, dY, ids, A, B, s)]
+        assert [torch.equal(a, b) for a, b in zip(again, first)] == [True] * 4
+    q.check()
+    _hold(first[0], *multi_ref.forward(W, x, ids, A, B, s), K, n, False, "h")
+    _hold(first[1], *multi_ref.backward(W, x, dY, ids, A, B, s)[0], N, n, False, "dX")
+
+
 @pytest.mark.parametrize("kind", ["nf4", "dense"])
 def test_broken_adapters_in_a_cut_last_wave(kind):
     # two of 40 adapters hold infinities, which land in chunks of different slices: their own tokens
